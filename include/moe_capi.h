@@ -228,6 +228,44 @@ int moe_dequant_rows_scaled(const moe_config* cfg, const uint8_t* codes, const v
                             const float* row_scales, int32_t row0, int32_t rows, int32_t cols, float* out,
                             void* stream);
 
+/* ---- Dense operators ----------------------------------------------------
+ * What a model has around the MoE layer: products with one packed matrix
+ * (projections, a vocabulary head, the serving form of a dense gated block)
+ * and the dense gated feed-forward block in 16 bits with its gradients (what
+ * is tuned before it is packed).  The pages have no counterpart.  They follow
+ * the conventions above: asynchronous on `stream`, checked on the host, no
+ * allocation, the same bits for the same inputs. */
+typedef enum moe_type { MOE_BF16 = 0, MOE_FP16 = 1, MOE_FP32 = 2 } moe_type;
+
+/* y[t][n] = sum_k W[n][k] x[t][k] (+ bias[n]) for a packed matrix W of `rows`
+ * rows and `cols` columns, in the format that cfg's bits, block, half_levels
+ * and scale_fmt name (the other fields are not looked at): 4-bit codes with
+ * one fp16 scale per 32 or 128 elements, integer or half-integer levels, or
+ * one E4M3 byte per 32 under row_scales[rows] (fp32; NULL for the fp16
+ * formats).  x: [T][cols], x_type MOE_BF16 or MOE_FP16; y: [T][rows], y_type
+ * any moe_type; bias: [rows] fp32 or NULL.  codes, scales, row_scales, x and y
+ * are dense and 16-byte aligned; x and y may not overlap.  Any rows >= 1, any
+ * T (meant for decode batches: T > 32 is cut into slices that each read the
+ * weights); cols a multiple of the block, at most 32768.  Products and sums
+ * are fp32, rounded once to y_type; the activations are taken exactly but for
+ * elements smaller than 2^-31 of their row's largest magnitude, which are off
+ * by at most 2^-35 of it.  A row of x that holds an infinity or a NaN gives a
+ * row of NaN.  The call reads the weights before it waits for a kernel ahead
+ * of it that lets its dependents launch early; none in this library writes
+ * weights. */
+int moe_linear_forward(const moe_config* cfg, const uint8_t* codes, const void* scales, const float* row_scales,
+                       int32_t rows, int32_t cols, const float* bias, const void* x, int32_t x_type, int32_t T,
+                       void* y, int32_t y_type, void* stream);
+
+/* h[t][i] = silu(z[t][2i]) * z[t][2i+1], z = W x as above without bias, for a
+ * packed matrix of 2 * inter rows laid out like an expert's gate/up matrix
+ * (row 2i = gate row i, row 2i+1 = up row i): both projections, the activation
+ * and the product of a gated feed-forward block in one launch.  h: [T][inter].
+ * moe_linear_forward with the down matrix completes the block. */
+int moe_linear_gated_forward(const moe_config* cfg, const uint8_t* codes, const void* scales,
+                             const float* row_scales, int32_t inter, int32_t cols, const void* x, int32_t x_type,
+                             int32_t T, void* h, int32_t h_type, void* stream);
+
 /* Measurement hook.  moe_profile_begin(n) makes the next n layer calls
  * record CUDA events around their four phases on the call's stream (route,
  * gate/up + SwiGLU, down, combine); moe_profile_end() waits for those events

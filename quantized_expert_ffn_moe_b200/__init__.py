@@ -23,6 +23,7 @@ __all__ = [
     "moe_profile_begin",
     "moe_profile_end", "moe_layer_forward_noalloc", "moe_noalloc_device_status", "NOALLOC_SCRATCH_BYTES",
     "moe_layer_forward_ep", "ep_all_reduce",
+    "MOE_BF16", "MOE_FP16", "MOE_FP32", "linear_config_of", "moe_linear_forward", "moe_linear_gated_forward",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libmoe.so")
@@ -31,9 +32,11 @@ EXPORTS = ("moe_workspace_bytes", "moe_route", "moe_layer_forward", "moe_stack_f
            "moe_device_status", "moe_dequant_rows", "moe_status_str", "moe_profile_begin", "moe_profile_end",
            "moe_layer_forward_noalloc", "moe_last_cuda_error", "moe_debug_fused_timing",
            "moe_debug_prefill_timing", "moe_layer_forward_ep", "moe_debug_decode_path", "moe_debug_wait_probe",
-           "moe_noalloc_device_status", "moe_dequant_rows_scaled")
+           "moe_noalloc_device_status", "moe_dequant_rows_scaled", "moe_linear_forward",
+           "moe_linear_gated_forward")
 
 MOE_OK = 0
+MOE_BF16, MOE_FP16, MOE_FP32 = 0, 1, 2      # moe_type
 
 
 class MoeError(RuntimeError):
@@ -119,6 +122,10 @@ def load_library(path: str = LIB_PATH):
     lib.moe_layer_forward_noalloc.restype = ctypes.c_int
     lib.moe_noalloc_device_status.argtypes = [ctypes.POINTER(ctypes.c_int32)]
     lib.moe_noalloc_device_status.restype = ctypes.c_int
+    lib.moe_linear_forward.argtypes = [cfgp, P, P, P, I32, I32, P, P, I32, I32, P, I32, P]
+    lib.moe_linear_forward.restype = ctypes.c_int
+    lib.moe_linear_gated_forward.argtypes = [cfgp, P, P, P, I32, I32, P, I32, I32, P, I32, P]
+    lib.moe_linear_gated_forward.restype = ctypes.c_int
     lib.moe_profile_begin.argtypes = [I32]
     lib.moe_profile_begin.restype = ctypes.c_int
     lib.moe_profile_end.argtypes = [ctypes.POINTER(ctypes.c_float), ctypes.POINTER(ctypes.c_int32)]
@@ -279,6 +286,93 @@ def moe_dequant_rows_scaled(cfg: MoeConfig, codes, scales, row_scales, row0: int
                                                 row0, rows, cols, _ptr(out), _stream(stream))
     if check:
         _check(st, "moe_dequant_rows_scaled")
+    return st
+
+
+# ------------------------------------------------------- dense operators ---
+def linear_config_of(bits=4, block=32, half_levels=False, fp8_scales=False) -> MoeConfig:
+    """The config of one packed matrix: the format fields alone (the sizes come
+    from the tensors)."""
+    return MoeConfig(bits=bits, block=block, half_levels=1 if half_levels else 0, scale_fmt=1 if fp8_scales else 0)
+
+
+def _dense(what: str, device, **tensors):
+    """Every given tensor dense and on `device`; the C entry sees only pointers."""
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        if t.device != device:
+            raise ValueError(f"{what}: {name} is on {t.device}, x on {device}")
+        if not t.is_contiguous():
+            raise ValueError(f"{what}: {name} is not contiguous")
+
+
+def _type_of(what: str, name: str, t, fp32: bool = False) -> int:
+    import torch
+    code = {torch.bfloat16: MOE_BF16, torch.float16: MOE_FP16, torch.float32: MOE_FP32 if fp32 else None}.get(t.dtype)
+    if code is None:
+        raise ValueError(f"{what}: {name} has type {t.dtype}")
+    return code
+
+
+def _on_device(device, stream, call):
+    """call(stream handle) with `device` current; without a stream, on that
+    device's current stream."""
+    import torch
+    if device.type != "cuda":
+        raise ValueError(f"x is on {device}: a CUDA tensor is needed")
+    if device.index == torch.cuda.current_device():
+        return call(_stream(stream))
+    with torch.cuda.device(device):
+        return call(_stream(stream))
+
+
+def _packed(what: str, cfg: MoeConfig, codes, scales, row_scales, rows: int, cols: int):
+    if codes.numel() * codes.element_size() * 2 != rows * cols:
+        raise ValueError(f"{what}: codes hold {codes.numel() * codes.element_size() * 2} elements, not {rows} x {cols}")
+    if cfg.block <= 0 or cols % cfg.block:
+        raise MoeError(-2, what)
+    if scales.numel() * scales.element_size() != rows * (cols // cfg.block) * (1 if cfg.scale_fmt == 1 else 2):
+        raise ValueError(f"{what}: scales do not fit {rows} x {cols // cfg.block} blocks")
+    if row_scales is not None and (row_scales.numel() != rows or row_scales.element_size() != 4):
+        raise ValueError(f"{what}: row_scales are not {rows} fp32 values")
+
+
+def moe_linear_forward(cfg: MoeConfig, codes, scales, x, y, *, row_scales=None, bias=None, stream=None,
+                       check=True) -> int:
+    """y [T][rows] = x [T][cols] times the packed matrix's transpose (+ bias
+    [rows] fp32).  x bf16 or fp16; y bf16, fp16 or fp32."""
+    what = "moe_linear_forward"
+    _dense(what, x.device, codes=codes, scales=scales, x=x, y=y, row_scales=row_scales, bias=bias)
+    (T, cols), rows = x.shape, y.shape[-1]
+    if y.shape != (T, rows):
+        raise ValueError(f"{what}: y is {tuple(y.shape)} for {T} rows of x")
+    _packed(what, cfg, codes, scales, row_scales, rows, cols)
+    if bias is not None and (bias.numel() != rows or bias.element_size() != 4):
+        raise ValueError(f"{what}: bias is not {rows} fp32 values")
+    xt, yt = _type_of(what, "x", x), _type_of(what, "y", y, fp32=True)
+    st = _on_device(x.device, stream, lambda s: load_library().moe_linear_forward(
+        ctypes.byref(cfg), _ptr(codes), _ptr(scales), _ptr(row_scales), rows, cols, _ptr(bias), _ptr(x), xt, T,
+        _ptr(y), yt, s))
+    if check:
+        _check(st, what)
+    return st
+
+
+def moe_linear_gated_forward(cfg: MoeConfig, codes, scales, x, h, *, row_scales=None, stream=None, check=True) -> int:
+    """h [T][I] = silu(x W_gate^T) * (x W_up^T) for a packed matrix of 2I rows,
+    row 2i = gate row i, row 2i + 1 = up row i."""
+    what = "moe_linear_gated_forward"
+    _dense(what, x.device, codes=codes, scales=scales, x=x, h=h, row_scales=row_scales)
+    (T, cols), inter = x.shape, h.shape[-1]
+    if h.shape != (T, inter):
+        raise ValueError(f"{what}: h is {tuple(h.shape)} for {T} rows of x")
+    _packed(what, cfg, codes, scales, row_scales, 2 * inter, cols)
+    xt, ht = _type_of(what, "x", x), _type_of(what, "h", h, fp32=True)
+    st = _on_device(x.device, stream, lambda s: load_library().moe_linear_gated_forward(
+        ctypes.byref(cfg), _ptr(codes), _ptr(scales), _ptr(row_scales), inter, cols, _ptr(x), xt, T, _ptr(h), ht, s))
+    if check:
+        _check(st, what)
     return st
 
 

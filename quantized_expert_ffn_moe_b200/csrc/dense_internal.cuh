@@ -1,0 +1,39 @@
+// Internal declarations of the dense operators: products with one packed
+// matrix (linear.cu) and the 16-bit gated feed-forward block (ffn.cu).
+#pragma once
+
+#include "moe_internal.cuh"
+
+namespace moe {
+
+// Columns a packed product takes at most: one token's activations (2 bytes a
+// column), the blocks' initial sums (1 byte a column) and the weight ring
+// share one SM's shared memory.
+constexpr int kLinearMaxCols = 32768;
+
+struct LinearCall {
+  const uint8_t* codes;
+  const void* scales;
+  const float* row_scales;
+  const float* bias;
+  const void* x;
+  void* y;
+  int rows, cols, T;      // rows of the packed matrix (2I when gated)
+  int block, half_levels, scale_fmt;
+  int x_type, y_type, gated;
+};
+
+cudaError_t launch_linear(const LinearCall& c, int num_sms, cudaStream_t s);
+
+// moe_capi.cu
+int num_sms_of_current_device();
+int status_of_cuda(cudaError_t e);
+
+// One value rounded to a moe_type and stored at index `at`.
+__device__ __forceinline__ void store_as(void* p, int type, size_t at, float v) {
+  if (type == MOE_FP32) static_cast<float*>(p)[at] = v;
+  else if (type == MOE_BF16) static_cast<__nv_bfloat16*>(p)[at] = __float2bfloat16_rn(v);
+  else static_cast<__half*>(p)[at] = __float2half_rn(v);
+}
+
+}  // namespace moe

@@ -1,7 +1,6 @@
 // C ABI of libmoe.so: argument validation and launch sequencing.  The
 // operation and the conventions are documented in include/moe_capi.h.
-#include "moe_internal.cuh"
-
+#include "dense_internal.cuh"
 
 namespace moe {
 cudaError_t launch_route_full(const moe_config& c, const uint16_t* router_w, const float* bias,
@@ -129,6 +128,9 @@ int run_layer(const LayerArgs& a) {
 }  // namespace
 
 namespace moe {
+int num_sms_of_current_device() { return num_sms_current(); }
+int status_of_cuda(cudaError_t e) { return cuda_status(e); }
+
 // Everything moe_layer_forward checks before it looks at the workspace, in the
 // same order: the config, T, the weights, x and y (non-null, 16-byte aligned,
 // not overlapping).  T == 0 passes (the call is then a no-op).
