@@ -266,6 +266,37 @@ int moe_linear_gated_forward(const moe_config* cfg, const uint8_t* codes, const 
                              const float* row_scales, int32_t inter, int32_t cols, const void* x, int32_t x_type,
                              int32_t T, void* h, int32_t h_type, void* stream);
 
+/* The dense gated feed-forward block on 16-bit weights (type MOE_BF16 or
+ * MOE_FP16 for every array; what is tuned before it is packed):
+ *   g = x Wg^T, u = x Wu^T, h = silu(g) * u, y = h Wd^T
+ *   w_gate_up [2 inter][hidden], row 2i = gate row i, row 2i+1 = up row i
+ *   w_down    [hidden][inter],  x, y [T][hidden]
+ * All arrays dense, row-major, 16-byte aligned; y overlaps nothing.  hidden and
+ * inter multiples of 8, at most 65536; any T >= 0 up to 2^22.  g, u and every
+ * sum are fp32; h is rounded to 16 bits between the two products and y once.
+ * The workspace (256-byte aligned, moe_ffn_workspace_bytes) holds h; its first
+ * words are the device check that moe_device_status reads. */
+int moe_ffn_forward(int32_t hidden, int32_t inter, int32_t type, const void* w_gate_up, const void* w_down,
+                    const void* x, int32_t T, void* y, void* workspace, size_t ws_bytes, void* stream);
+
+/* Gradients of moe_ffn_forward for the output's gradient dy [T][hidden]:
+ *   dh = dy Wd, s = sigmoid(g), a = g s, du = dh a, dg = dh u (s + a (1 - s))
+ *   dx = dg Wg + du Wu [T][hidden], dw_gate_up (laid out like w_gate_up),
+ *   dw_down = dy^T h [hidden][inter]
+ * from x, dy and the weights alone: the projections are computed again, so the
+ * forward call keeps nothing.  An output that is NULL is not computed.  Outputs
+ * are overwritten (no accumulation) and overlap nothing.  dg, du and h are
+ * rounded to 16 bits between the products, everything else is fp32.  T == 0
+ * clears the weight gradients. */
+int moe_ffn_backward(int32_t hidden, int32_t inter, int32_t type, const void* w_gate_up, const void* w_down,
+                     const void* x, const void* dy, int32_t T, void* dx, void* dw_gate_up, void* dw_down,
+                     void* workspace, size_t ws_bytes, void* stream);
+
+/* Bytes of device workspace of the two calls above for up to max_tokens
+ * tokens (the forward's, or with backward != 0 enough for either); 0 for sizes
+ * they refuse. */
+size_t moe_ffn_workspace_bytes(int32_t hidden, int32_t inter, int32_t max_tokens, int32_t backward);
+
 /* Measurement hook.  moe_profile_begin(n) makes the next n layer calls
  * record CUDA events around their four phases on the call's stream (route,
  * gate/up + SwiGLU, down, combine); moe_profile_end() waits for those events

@@ -24,6 +24,7 @@ __all__ = [
     "moe_profile_end", "moe_layer_forward_noalloc", "moe_noalloc_device_status", "NOALLOC_SCRATCH_BYTES",
     "moe_layer_forward_ep", "ep_all_reduce",
     "MOE_BF16", "MOE_FP16", "MOE_FP32", "linear_config_of", "moe_linear_forward", "moe_linear_gated_forward",
+    "moe_ffn_workspace_bytes", "moe_ffn_forward", "moe_ffn_backward",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libmoe.so")
@@ -33,7 +34,7 @@ EXPORTS = ("moe_workspace_bytes", "moe_route", "moe_layer_forward", "moe_stack_f
            "moe_layer_forward_noalloc", "moe_last_cuda_error", "moe_debug_fused_timing",
            "moe_debug_prefill_timing", "moe_layer_forward_ep", "moe_debug_decode_path", "moe_debug_wait_probe",
            "moe_noalloc_device_status", "moe_dequant_rows_scaled", "moe_linear_forward",
-           "moe_linear_gated_forward")
+           "moe_linear_gated_forward", "moe_ffn_workspace_bytes", "moe_ffn_forward", "moe_ffn_backward")
 
 MOE_OK = 0
 MOE_BF16, MOE_FP16, MOE_FP32 = 0, 1, 2      # moe_type
@@ -126,6 +127,12 @@ def load_library(path: str = LIB_PATH):
     lib.moe_linear_forward.restype = ctypes.c_int
     lib.moe_linear_gated_forward.argtypes = [cfgp, P, P, P, I32, I32, P, I32, I32, P, I32, P]
     lib.moe_linear_gated_forward.restype = ctypes.c_int
+    lib.moe_ffn_workspace_bytes.argtypes = [I32, I32, I32, I32]
+    lib.moe_ffn_workspace_bytes.restype = SZ
+    lib.moe_ffn_forward.argtypes = [I32, I32, I32, P, P, P, I32, P, P, SZ, P]
+    lib.moe_ffn_forward.restype = ctypes.c_int
+    lib.moe_ffn_backward.argtypes = [I32, I32, I32, P, P, P, P, I32, P, P, P, P, SZ, P]
+    lib.moe_ffn_backward.restype = ctypes.c_int
     lib.moe_profile_begin.argtypes = [I32]
     lib.moe_profile_begin.restype = ctypes.c_int
     lib.moe_profile_end.argtypes = [ctypes.POINTER(ctypes.c_float), ctypes.POINTER(ctypes.c_int32)]
@@ -371,6 +378,54 @@ def moe_linear_gated_forward(cfg: MoeConfig, codes, scales, x, h, *, row_scales=
     xt, ht = _type_of(what, "x", x), _type_of(what, "h", h, fp32=True)
     st = _on_device(x.device, stream, lambda s: load_library().moe_linear_gated_forward(
         ctypes.byref(cfg), _ptr(codes), _ptr(scales), _ptr(row_scales), inter, cols, _ptr(x), xt, T, _ptr(h), ht, s))
+    if check:
+        _check(st, what)
+    return st
+
+
+def moe_ffn_workspace_bytes(hidden: int, inter: int, max_tokens: int, backward: bool = False) -> int:
+    return int(load_library().moe_ffn_workspace_bytes(hidden, inter, max_tokens, 1 if backward else 0))
+
+
+def _ffn_sizes(what: str, w_gate_up, w_down, x, **others):
+    """(hidden, inter, T, type) of a block, every array checked against them."""
+    hidden, inter = w_down.shape
+    T = x.shape[0]
+    want = {"w_gate_up": (2 * inter, hidden), "x": (T, hidden), "y": (T, hidden), "dy": (T, hidden),
+            "dx": (T, hidden), "dw_gate_up": (2 * inter, hidden), "dw_down": (hidden, inter)}
+    arrays = {"w_gate_up": w_gate_up, "x": x, **others}
+    for name, t in arrays.items():
+        if t is not None and (tuple(t.shape) != want[name] or t.dtype != x.dtype):
+            raise ValueError(f"{what}: {name} is {tuple(t.shape)} of {t.dtype}, not {want[name]} of {x.dtype}")
+    if w_down.dtype != x.dtype:
+        raise ValueError(f"{what}: w_down has type {w_down.dtype}, x {x.dtype}")
+    return hidden, inter, T, _type_of(what, "x", x)
+
+
+def moe_ffn_forward(w_gate_up, w_down, x, y, workspace, *, stream=None, check=True) -> int:
+    """y [T][H] = (silu(x Wg^T) * (x Wu^T)) Wd^T on 16-bit weights: w_gate_up
+    [2I][H] with gate and up rows interleaved, w_down [H][I]."""
+    what = "moe_ffn_forward"
+    _dense(what, x.device, w_gate_up=w_gate_up, w_down=w_down, x=x, y=y, workspace=workspace)
+    hidden, inter, T, ty = _ffn_sizes(what, w_gate_up, w_down, x, y=y)
+    st = _on_device(x.device, stream, lambda s: load_library().moe_ffn_forward(
+        hidden, inter, ty, _ptr(w_gate_up), _ptr(w_down), _ptr(x), T, _ptr(y), _ptr(workspace), _nbytes(workspace), s))
+    if check:
+        _check(st, what)
+    return st
+
+
+def moe_ffn_backward(w_gate_up, w_down, x, dy, workspace, *, dx=None, dw_gate_up=None, dw_down=None, stream=None,
+                     check=True) -> int:
+    """Gradients of moe_ffn_forward for dy [T][H]; the ones given as tensors are
+    overwritten, the others are not computed."""
+    what = "moe_ffn_backward"
+    _dense(what, x.device, w_gate_up=w_gate_up, w_down=w_down, x=x, dy=dy, workspace=workspace, dx=dx,
+           dw_gate_up=dw_gate_up, dw_down=dw_down)
+    hidden, inter, T, ty = _ffn_sizes(what, w_gate_up, w_down, x, dy=dy, dx=dx, dw_gate_up=dw_gate_up, dw_down=dw_down)
+    st = _on_device(x.device, stream, lambda s: load_library().moe_ffn_backward(
+        hidden, inter, ty, _ptr(w_gate_up), _ptr(w_down), _ptr(x), _ptr(dy), T, _ptr(dx), _ptr(dw_gate_up),
+        _ptr(dw_down), _ptr(workspace), _nbytes(workspace), s))
     if check:
         _check(st, what)
     return st

@@ -47,6 +47,41 @@ int run_linear(LinearCall& c, const moe_config* cfg, int out_cols, void* stream)
   return status_of_cuda(launch_linear(c, num_sms_of_current_device(), static_cast<cudaStream_t>(stream)));
 }
 
+int check_ffn_shape(int H, int I, int type, int T) {
+  if (H <= 0 || I <= 0 || T < 0 || (type != MOE_BF16 && type != MOE_FP16)) return MOE_ERR_INVALID_ARG;
+  // rows on 16-byte boundaries; sizes whose products stay inside the tensor copies' and tile counts' range
+  if (H % 8 != 0 || I % 8 != 0 || H > kFfnMaxSize || I > kFfnMaxSize || T > kFfnMaxTokens) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+struct Span {
+  const void* p;
+  size_t bytes;
+};
+
+// Inputs: required.  Outputs: may be null where `optional`; overlap with no
+// input, no other output and not with the workspace.
+int check_ffn_pointers(const Span* in, int n_in, const Span* out, int n_out, bool optional, const Span& ws,
+                       size_t ws_need) {
+  for (int i = 0; i < n_in; ++i)
+    if (!in[i].p || !aligned(in[i].p, 16)) return MOE_ERR_INVALID_ARG;
+  for (int i = 0; i < n_out; ++i) {
+    if (!out[i].p && !optional) return MOE_ERR_INVALID_ARG;
+    if (!aligned(out[i].p, 16)) return MOE_ERR_INVALID_ARG;
+    for (int j = 0; out[i].p && j < n_in; ++j)
+      if (overlap(out[i].p, out[i].bytes, in[j].p, in[j].bytes)) return MOE_ERR_INVALID_ARG;
+    for (int j = 0; out[i].p && j < i; ++j)
+      if (out[j].p && overlap(out[i].p, out[i].bytes, out[j].p, out[j].bytes)) return MOE_ERR_INVALID_ARG;
+  }
+  if (!ws.p || !aligned(ws.p, 256)) return MOE_ERR_INVALID_ARG;
+  if (ws.bytes < ws_need) return MOE_ERR_WORKSPACE;
+  for (int i = 0; i < n_in; ++i)
+    if (overlap(in[i].p, in[i].bytes, ws.p, ws_need)) return MOE_ERR_INVALID_ARG;
+  for (int i = 0; i < n_out; ++i)
+    if (out[i].p && overlap(out[i].p, out[i].bytes, ws.p, ws_need)) return MOE_ERR_INVALID_ARG;
+  return MOE_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -69,6 +104,50 @@ int moe_linear_gated_forward(const moe_config* cfg, const uint8_t* codes, const 
   c.codes = codes; c.scales = scales; c.row_scales = row_scales; c.x = x; c.y = h;
   c.rows = 2 * inter; c.cols = cols; c.T = T; c.x_type = x_type; c.y_type = h_type; c.gated = 1;
   return run_linear(c, cfg, inter, stream);
+}
+
+size_t moe_ffn_workspace_bytes(int32_t hidden, int32_t inter, int32_t max_tokens, int32_t backward) {
+  if (check_ffn_shape(hidden, inter, MOE_BF16, max_tokens) != MOE_OK) return 0;
+  return ffn_workspace_bytes(hidden, inter, max_tokens, backward != 0);
+}
+
+int moe_ffn_forward(int32_t hidden, int32_t inter, int32_t type, const void* w_gate_up, const void* w_down,
+                    const void* x, int32_t T, void* y, void* workspace, size_t ws_bytes, void* stream) {
+  int st = check_ffn_shape(hidden, inter, type, T);
+  if (st != MOE_OK || T == 0) return st;
+  const size_t wb = size_t(hidden) * inter * 2, tb = size_t(T) * hidden * 2;
+  const Span in[] = {{w_gate_up, 2 * wb}, {w_down, wb}, {x, tb}};
+  const Span out[] = {{y, tb}};
+  st = check_ffn_pointers(in, 3, out, 1, false, {workspace, ws_bytes}, ffn_workspace_bytes(hidden, inter, T, false));
+  if (st != MOE_OK) return st;
+  FfnCall c{};
+  c.H = hidden; c.I = inter; c.T = T; c.type = type; c.w_gate_up = w_gate_up; c.w_down = w_down; c.x = x; c.y = y;
+  c.ws = workspace;
+  return status_of_cuda(launch_ffn_forward(c, num_sms_of_current_device(), static_cast<cudaStream_t>(stream)));
+}
+
+int moe_ffn_backward(int32_t hidden, int32_t inter, int32_t type, const void* w_gate_up, const void* w_down,
+                     const void* x, const void* dy, int32_t T, void* dx, void* dw_gate_up, void* dw_down,
+                     void* workspace, size_t ws_bytes, void* stream) {
+  int st = check_ffn_shape(hidden, inter, type, T);
+  if (st != MOE_OK) return st;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const size_t wb = size_t(hidden) * inter * 2, tb = size_t(T) * hidden * 2;
+  if (T == 0) {                                        // a sum over no tokens
+    if (!aligned(dw_gate_up, 16) || !aligned(dw_down, 16)) return MOE_ERR_INVALID_ARG;
+    cudaError_t e = cudaSuccess;
+    if (dw_gate_up) e = cudaMemsetAsync(dw_gate_up, 0, 2 * wb, s);
+    if (e == cudaSuccess && dw_down) e = cudaMemsetAsync(dw_down, 0, wb, s);
+    return status_of_cuda(e);
+  }
+  const Span in[] = {{w_gate_up, 2 * wb}, {w_down, wb}, {x, tb}, {dy, tb}};
+  const Span out[] = {{dx, tb}, {dw_gate_up, 2 * wb}, {dw_down, wb}};
+  st = check_ffn_pointers(in, 4, out, 3, true, {workspace, ws_bytes}, ffn_workspace_bytes(hidden, inter, T, true));
+  if (st != MOE_OK || (!dx && !dw_gate_up && !dw_down)) return st;
+  FfnCall c{};
+  c.H = hidden; c.I = inter; c.T = T; c.type = type; c.w_gate_up = w_gate_up; c.w_down = w_down; c.x = x; c.dy = dy;
+  c.dx = dx; c.dw_gate_up = dw_gate_up; c.dw_down = dw_down; c.ws = workspace;
+  return status_of_cuda(launch_ffn_backward(c, num_sms_of_current_device(), s));
 }
 
 }  // extern "C"

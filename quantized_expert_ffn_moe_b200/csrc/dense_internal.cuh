@@ -11,6 +11,10 @@ namespace moe {
 // share one SM's shared memory.
 constexpr int kLinearMaxCols = 32768;
 
+// Sizes of the 16-bit block: tile counts and coordinates fit 32 bits.
+constexpr int kFfnMaxSize = 65536;
+constexpr int kFfnMaxTokens = 1 << 22;
+
 struct LinearCall {
   const uint8_t* codes;
   const void* scales;
@@ -24,6 +28,23 @@ struct LinearCall {
 };
 
 cudaError_t launch_linear(const LinearCall& c, int num_sms, cudaStream_t s);
+
+struct FfnCall {
+  int H, I, T, type;
+  const void* w_gate_up;      // [2I][H]
+  const void* w_down;         // [H][I]
+  const void* x;              // [T][H]
+  const void* dy;             // [T][H]
+  void* y;                    // forward: [T][H]
+  void* dx;                   // [T][H], or null
+  void* dw_gate_up;           // [2I][H], or null
+  void* dw_down;              // [H][I], or null
+  void* ws;
+};
+
+size_t ffn_workspace_bytes(int H, int I, int T, bool backward);
+cudaError_t launch_ffn_forward(const FfnCall& c, int num_sms, cudaStream_t s);
+cudaError_t launch_ffn_backward(const FfnCall& c, int num_sms, cudaStream_t s);
 
 // moe_capi.cu
 int num_sms_of_current_device();

@@ -1,0 +1,792 @@
+// Dense gated feed-forward block on 16-bit weights and its gradients, on the
+// tcgen05 tensor cores.
+//
+//   g = x Wg^T, u = x Wu^T, h = silu(g) * u, y = h Wd^T
+//   dh = dy Wd;  s = sigmoid(g), a = g s;  du = dh a;  dg = dh u (s + a (1 - s))
+//   dx = dg Wg + du Wu;  dWg = dg^T x;  dWu = du^T x;  dWd = dy^T h
+//
+// with the gate and up rows interleaved in one matrix Wgu (row 2i gate, 2i + 1
+// up), so that an accumulator tile holds g and u of the same element in
+// neighbouring columns of a thread's row.  Forward: two launches (gate/up with
+// the activation and the product in the epilogue, down).  Backward: two
+// launches (the projections recomputed and dh side by side in tensor memory,
+// h and dgu = (dg, du) from their epilogue; then dx, dWgu and dWd as one list
+// of tiles).  g, u, dh and every sum stay fp32; h and dgu are rounded to 16
+// bits once because they are operands of the next tensor-core product, which
+// adds an error of the size of the output's own rounding.  Recomputing g and u
+// instead of storing them costs 4 of the 16 T H I products and saves 8 bytes
+// of fp32 a token and column; 16-bit copies of them would add their rounding
+// to every gradient.
+//
+// One persistent kernel per launch.  A tile is 256 x 256 on a pair of SMs
+// (cta_group::2: each brings its 128 rows of A and half of B's columns, so the
+// pair reads 64 KB per 64-deep step instead of 96) or, when there are too few
+// of those to occupy the machine, 128 x 64 on one SM.  Operands come by tensor
+// copies in the 128-byte swizzle, either contiguous along the reduction or
+// along the row (transposed operands are never copied: the instruction reads
+// both).  Roles: epilogue warps, one producer, one issuer; two accumulators,
+// so that a tile's epilogue runs under the next one's products.
+#include "dense_internal.cuh"
+#include "tensor_core.cuh"
+
+namespace moe {
+
+namespace {
+
+constexpr int BK = 64;                           // reduction depth of a stage: one 128-byte swizzle row
+constexpr int kAStage = 128 * 128;               // 128 rows x 64 deep x 2 bytes
+constexpr int kMaxStages = 8;
+constexpr int kBarArea = 512;
+
+// Tile shapes.  BN: columns of a tile; CG: SMs that share it.
+template <int CG, int BN>
+struct Tile {
+  static constexpr int BM = 128 * CG;
+  static constexpr int BROWS = BN / CG;          // columns that one SM brings
+  static constexpr int B_STAGE = BROWS * 128;
+  static constexpr int STAGE = kAStage + B_STAGE;
+  static constexpr int STAGES = 196608 / STAGE > kMaxStages ? kMaxStages : 196608 / STAGE;
+  static constexpr size_t SMEM = 1024 + size_t(STAGES) * STAGE + kBarArea;
+};
+
+// One product D[M][N] = A B^T.  a_mn / b_mn: the operand is contiguous along
+// its own rows (M or N) instead of along the reduction.
+struct Problem {
+  int M, N, kblocks;
+  int tiles_m, tiles_n, tile0;
+  int a_mn, b_mn;
+  void* out;
+  int ld;
+};
+struct GemmArgs {
+  Problem p[3];
+  int n, ntiles;
+  int bf16;
+  int reset;             // 1: the call's first launch clears the status words
+  int* status;
+};
+struct GemmMaps {
+  CUtensorMap a[3], b[3];
+};
+
+// ------------------------------------------------------------ primitives
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// Cluster address of the pair's first SM's copy of a shared-memory location.
+__device__ __forceinline__ uint32_t in_leader(const void* p) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(a) : "r"(smem_u32(p)));
+  return a;
+}
+template <int CG>
+__device__ __forceinline__ void arrive_leader(uint64_t* bar) {
+  if (CG == 1) mbar_arrive(bar);
+  else asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(in_leader(bar)) : "memory");
+}
+// Tensor copy into this SM's shared memory, completing on `bar` (this SM's
+// barrier, or with a pair the first SM's).
+template <int CG>
+__device__ __forceinline__ void load_box(void* dst, const CUtensorMap* map, int c0, int c1, uint32_t bar) {
+  if (CG == 1)
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
+        ::"r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3}], [%4];"
+        ::"r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar)
+        : "memory");
+}
+template <int CG>
+__device__ __forceinline__ void commit(uint64_t* bar) {
+  if (CG == 1)
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
+                 : "memory");
+  else
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
+        ::"r"(smem_u32(bar)), "h"(uint16_t(3))
+        : "memory");
+}
+template <int CG>
+__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  if (CG == 1)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+        ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+        ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+template <int CG>
+__device__ __forceinline__ void tmem_alloc(uint32_t* slot, uint32_t cols) {
+  if (CG == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(slot)), "r"(cols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  } else {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(slot)), "r"(cols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+}
+template <int CG>
+__device__ __forceinline__ void tmem_free(uint32_t base, uint32_t cols) {
+  if (CG == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(base), "r"(cols) : "memory");
+  else asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(base), "r"(cols) : "memory");
+}
+// 16 consecutive columns of this thread's tensor-memory lane.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t v[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+        "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+      : "r"(taddr));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+
+// Operand descriptor.  Contiguous along the reduction: sw128_desc (8-row atoms
+// 1024 bytes apart, 16 deep = 32 bytes on).  Contiguous along the rows: boxes
+// of 64 rows (128 bytes) x 64 deep, 8 KB apart; 8-deep atoms 1024 bytes apart,
+// 16 deep = 2048 bytes on.
+__device__ __forceinline__ uint64_t operand_desc(uint32_t saddr, int mn) {
+  const uint64_t d = sw128_desc(saddr);
+  return mn ? (d & ~(uint64_t(0x3FFF) << 16)) | (uint64_t(8192 >> 4) << 16) : d;
+}
+// fp32 accumulator, bf16 or fp16 operands, M x N, operand orders.
+__device__ __forceinline__ uint32_t instr_desc(int bf16, int a_mn, int b_mn, int m, int n) {
+  return (1u << 4) | (uint32_t(bf16) << 7) | (uint32_t(bf16) << 10) | (uint32_t(a_mn) << 15) | (uint32_t(b_mn) << 16) |
+         (uint32_t(n >> 3) << 17) | (uint32_t(m >> 4) << 24);
+}
+// The 64-deep step of one stage: four instructions.
+template <int CG>
+__device__ __forceinline__ void mma_stage(uint32_t d, uint32_t sa, uint32_t sb, int a_mn, int b_mn, uint32_t idesc,
+                                          bool first) {
+  const uint64_t ad = operand_desc(sa, a_mn), bd = operand_desc(sb, b_mn);
+  const uint32_t as = a_mn ? 2048 >> 4 : 32 >> 4, bs = b_mn ? 2048 >> 4 : 32 >> 4;
+#pragma unroll
+  for (int k = 0; k < BK / 16; ++k) mma<CG>(d, ad + k * as, bd + k * bs, idesc, (first && k == 0) ? 0u : 1u);
+}
+// One operand of a stage: `rows` rows from row0, 64 deep from k0.
+template <int CG>
+__device__ __forceinline__ void load_operand(unsigned char* dst, const CUtensorMap* map, int mn, int row0, int rows,
+                                             int k0, uint32_t bar) {
+  if (!mn) {
+    load_box<CG>(dst, map, k0, row0, bar);
+  } else {
+    for (int r = 0; r < rows; r += 64) load_box<CG>(dst + r * 128, map, row0 + r, k0, bar);
+  }
+}
+
+__device__ __forceinline__ uint32_t pack2(float a, float b, int bf16) {
+  if (bf16) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  }
+  return h2_as_u32(__floats2half2_rn(a, b));
+}
+// NV values of a row from column n (NV and the row's column count are
+// multiples of 8): 16-byte stores of the part inside the row.
+template <int NV>
+__device__ __forceinline__ void store_row(uint16_t* row, int n, int cols, const float (&v)[NV], int bf16) {
+#pragma unroll
+  for (int i = 0; i < NV; i += 8)
+    if (n + i < cols)
+      *reinterpret_cast<uint4*>(row + n + i) =
+          make_uint4(pack2(v[i], v[i + 1], bf16), pack2(v[i + 2], v[i + 3], bf16), pack2(v[i + 4], v[i + 5], bf16),
+                     pack2(v[i + 6], v[i + 7], bf16));
+}
+__device__ __forceinline__ float sigmoid(float g) { return __fdividef(1.f, 1.f + __expf(-g)); }
+
+// Tile l of a product: bands of 8 row tiles, column by column inside a band,
+// so that the tiles in flight share rows and columns in L2.
+__device__ __forceinline__ void tile_of(const Problem& p, int l, int* m, int* n) {
+  const int band = l / (8 * p.tiles_n), m0 = band * 8;
+  const int h = min(8, p.tiles_m - m0), r = l - band * 8 * p.tiles_n;
+  *m = m0 + r % h;
+  *n = r / h;
+}
+
+enum { EPI_STORE = 0, EPI_GATED = 1 };
+constexpr int kEpiWarps = 8;
+constexpr int kGemmThreads = (kEpiWarps + 2) * 32;
+
+// ------------------------------------------------------------ products
+// D = A B^T for up to three products, rounded and stored (EPI_STORE), or one
+// product whose column pairs (g, u) become silu(g) * u (EPI_GATED).
+template <int CG, int BN, int EPI>
+__global__ void __launch_bounds__(kGemmThreads, 1) ffn_gemm_kernel(const __grid_constant__ GemmArgs a,
+                                                                   const __grid_constant__ GemmMaps maps) {
+  using T = Tile<CG, BN>;
+  extern __shared__ __align__(1024) unsigned char fsm[];
+  unsigned char* base = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(fsm) + 1023) & ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(base + size_t(T::STAGES) * T::STAGE);
+  uint64_t* empty = full + kMaxStages;
+  uint64_t* acc_full = empty + kMaxStages;
+  uint64_t* acc_empty = acc_full + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_empty + 2);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  constexpr uint32_t kCols = 2 * BN < 32 ? 32 : 2 * BN;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = CG == 1 ? 0 : int(cluster_rank());
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < T::STAGES; ++i) { mbar_init(&full[i], 1); mbar_init(&empty[i], 1); }
+    for (int i = 0; i < 2; ++i) { mbar_init(&acc_full[i], 1); mbar_init(&acc_empty[i], CG * kEpiWarps); }
+    *abort_flag = 0;
+    mbar_fence_init();
+  }
+  if (warp == kEpiWarps + 1) tmem_alloc<CG>(tmem_slot, kCols);
+  __syncwarp();
+  tc_fence_before();
+  if (CG == 1) __syncthreads();
+  else cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  pdl_wait();
+  pdl_launch_dependents();
+  if (a.reset && blockIdx.x == 0 && threadIdx.x == 0) { a.status[0] = 0; a.status[1] = 0; }
+
+  const int unit = int(blockIdx.x) / CG, units = int(gridDim.x) / CG;
+  auto find = [&](int t, int* m, int* n) -> int {
+    int i = 0;
+    while (i + 1 < a.n && t >= a.p[i + 1].tile0) ++i;
+    tile_of(a.p[i], t - a.p[i].tile0, m, n);
+    return i;
+  };
+
+  if (warp == kEpiWarps && lane == 0) {
+    // ------------------------------------------------------- producer
+    int kc = 0;
+    for (int t = unit; t < a.ntiles && !*abort_flag; t += units) {
+      int m, n;
+      const int i = find(t, &m, &n);
+      const Problem& p = a.p[i];
+      for (int kb = 0; kb < p.kblocks; ++kb, ++kc) {
+        const int s = kc % T::STAGES;
+        if (kc >= T::STAGES && !mbar_wait(&empty[s], ((kc / T::STAGES) - 1) & 1, abort_flag)) {
+          *abort_flag = 1; report_error(a.status, MOE_ERR_TIMEOUT, 50); break;
+        }
+        unsigned char* st = base + size_t(s) * T::STAGE;
+        if (rank == 0) mbar_arrive_expect_tx(&full[s], CG * T::STAGE);
+        const uint32_t bar = CG == 1 ? smem_u32(&full[s]) : in_leader(&full[s]);
+        load_operand<CG>(st, &maps.a[i], p.a_mn, m * T::BM + rank * 128, 128, kb * BK, bar);
+        load_operand<CG>(st + kAStage, &maps.b[i], p.b_mn, n * BN + rank * T::BROWS, T::BROWS, kb * BK, bar);
+      }
+    }
+    // no copy and no release of a stage is under way when this SM leaves
+    for (int i = max(0, kc - T::STAGES); i < kc; ++i) {
+      const int s = i % T::STAGES;
+      bool ok = rank != 0 || mbar_wait(&full[s], (i / T::STAGES) & 1, nullptr);
+      ok = ok && (*abort_flag || mbar_wait(&empty[s], (i / T::STAGES) & 1, abort_flag));
+      if (!ok) report_error(a.status, MOE_ERR_TIMEOUT, 51);
+    }
+  } else if (warp == kEpiWarps + 1 && rank == 0) {
+    // --------------------------------------------------------- issuer
+    int kc = 0, tc = 0;
+    bool ok = true;
+    for (int t = unit; t < a.ntiles && ok; t += units, ++tc) {
+      if (__any_sync(0xffffffffu, *abort_flag != 0)) break;
+      int m, n;
+      const int i = find(t, &m, &n);
+      const Problem& p = a.p[i];
+      const int buf = tc & 1;
+      if (tc >= 2) ok = __all_sync(0xffffffffu, mbar_wait(&acc_empty[buf], ((tc >> 1) - 1) & 1, abort_flag));
+      if (!ok) {
+        if (lane == 0) { *abort_flag = 1; report_error(a.status, MOE_ERR_TIMEOUT, 52); }
+        break;
+      }
+      tc_fence_after();
+      const uint32_t idesc = instr_desc(a.bf16, p.a_mn, p.b_mn, T::BM, BN);
+      for (int kb = 0; kb < p.kblocks; ++kb, ++kc) {
+        const int s = kc % T::STAGES;
+        ok = __all_sync(0xffffffffu, mbar_wait(&full[s], (kc / T::STAGES) & 1, abort_flag));
+        if (!ok) {
+          if (lane == 0) { *abort_flag = 1; report_error(a.status, MOE_ERR_TIMEOUT, 53); }
+          break;
+        }
+        tc_fence_after();
+        const uint32_t sa = smem_u32(base + size_t(s) * T::STAGE);
+        if (elect_one()) {
+          mma_stage<CG>(tmem + uint32_t(buf * BN), sa, sa + kAStage, p.a_mn, p.b_mn, idesc, kb == 0);
+          commit<CG>(&empty[s]);
+          if (kb == p.kblocks - 1) commit<CG>(&acc_full[buf]);
+        }
+        __syncwarp();
+      }
+    }
+  } else if (warp < kEpiWarps) {
+    // ------------------------------------------------------- epilogue
+    const int q = warp & 3, half = warp >> 2;
+    constexpr int HC = BN / 2;                     // columns of this warp
+    int tc = 0;
+    for (int t = unit; t < a.ntiles; t += units, ++tc) {
+      int m, n;
+      const Problem& p = a.p[find(t, &m, &n)];
+      const int buf = tc & 1;
+      const bool ok = !*abort_flag && mbar_wait(&acc_full[buf], (tc >> 1) & 1, abort_flag);
+      if (!__all_sync(0xffffffffu, ok)) {
+        if (!*abort_flag) { *abort_flag = 1; report_error(a.status, MOE_ERR_TIMEOUT, 55); }
+        break;
+      }
+      tc_fence_after();
+      const int row = m * T::BM + rank * 128 + q * 32 + lane;
+      const uint32_t tq = tmem + (uint32_t(q * 32) << 16) + uint32_t(buf * BN + half * HC);
+      uint16_t* out = static_cast<uint16_t*>(p.out) + size_t(row) * p.ld;
+#pragma unroll
+      for (int c = 0; c < HC; c += 32) {
+        uint32_t v[32];
+        tmem_ld32(tq + c, v);
+        const int col = n * BN + half * HC + c;
+        if (row < p.M) {
+          if (EPI == EPI_STORE) {
+            float f[32];
+#pragma unroll
+            for (int j = 0; j < 32; ++j) f[j] = __uint_as_float(v[j]);
+            store_row<32>(out, col, p.ld, f, a.bf16);
+          } else {
+            float f[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              const float g = __uint_as_float(v[2 * j]), u = __uint_as_float(v[2 * j + 1]);
+              f[j] = g * sigmoid(g) * u;
+            }
+            store_row<16>(out, col >> 1, p.ld, f, a.bf16);
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) arrive_leader<CG>(&acc_empty[buf]);
+    }
+  }
+
+  __syncwarp();
+  tc_fence_before();
+  if (CG == 1) __syncthreads();
+  else cluster_sync();
+  if (warp == kEpiWarps + 1) {
+    tc_fence_after();
+    tmem_free<CG>(tmem, kCols);
+  }
+}
+
+// ------------------------------------------------- h and dgu of the backward
+struct GradArgs {
+  int T, H, I;
+  int tiles_m, tiles_n, kblocks;      // kblocks of one phase (the reduction over H)
+  int bf16, reset;
+  uint16_t* h;                        // [T][I], or null
+  uint16_t* dgu;                      // [T][2I]
+  int* status;
+};
+constexpr int kGradEpi = 16;
+constexpr int kGradThreads = (kGradEpi + 2) * 32;
+
+// One tile: 128 CG tokens x NI hidden elements.  First g and u (2 NI columns
+// of tensor memory, the reduction over H), then dh (NI columns, two buffers).
+// While dh's products run, the epilogue turns g and u into h (stored) and into
+// the factors of dh, du / dh = a and dg / dh = u (s + a (1 - s)), which it
+// keeps in registers: the g and u columns are free again for the next tile's
+// first products before dh is done.
+template <int CG, int NI>
+__global__ void __launch_bounds__(kGradThreads, 1) ffn_grad_kernel(const __grid_constant__ GradArgs a,
+                                                                   const __grid_constant__ CUtensorMap tm_x,
+                                                                   const __grid_constant__ CUtensorMap tm_wgu,
+                                                                   const __grid_constant__ CUtensorMap tm_dy,
+                                                                   const __grid_constant__ CUtensorMap tm_wd) {
+  using T = Tile<CG, 2 * NI>;
+  constexpr int DROWS = NI / CG;                  // Wd columns that one SM brings
+  constexpr int D_STAGE = kAStage + DROWS * 128;
+  static_assert(DROWS % 64 == 0, "Wd comes in boxes of 64 columns");
+  extern __shared__ __align__(1024) unsigned char fsm[];
+  unsigned char* base = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(fsm) + 1023) & ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(base + size_t(T::STAGES) * T::STAGE);
+  uint64_t* empty = full + kMaxStages;
+  uint64_t* gu_full = empty + kMaxStages;
+  uint64_t* gu_empty = gu_full + 1;
+  uint64_t* dh_full = gu_empty + 1;
+  uint64_t* dh_empty = dh_full + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(dh_empty + 2);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  constexpr uint32_t kCols = 4 * NI;              // g and u, then two of dh
+  static_assert((kCols & (kCols - 1)) == 0 && kCols <= 512, "tensor memory");
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = CG == 1 ? 0 : int(cluster_rank());
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < T::STAGES; ++i) { mbar_init(&full[i], 1); mbar_init(&empty[i], 1); }
+    mbar_init(gu_full, 1);
+    mbar_init(gu_empty, CG * kGradEpi);
+    for (int i = 0; i < 2; ++i) { mbar_init(&dh_full[i], 1); mbar_init(&dh_empty[i], CG * kGradEpi); }
+    *abort_flag = 0;
+    mbar_fence_init();
+  }
+  if (warp == kGradEpi + 1) tmem_alloc<CG>(tmem_slot, kCols);
+  __syncwarp();
+  tc_fence_before();
+  if (CG == 1) __syncthreads();
+  else cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  pdl_wait();
+  pdl_launch_dependents();
+  if (a.reset && blockIdx.x == 0 && threadIdx.x == 0) { a.status[0] = 0; a.status[1] = 0; }
+
+  const int unit = int(blockIdx.x) / CG, units = int(gridDim.x) / CG;
+  const int ntiles = a.tiles_m * a.tiles_n;
+  Problem shape{};
+  shape.tiles_m = a.tiles_m;
+  shape.tiles_n = a.tiles_n;
+
+  if (warp == kGradEpi && lane == 0) {
+    int kc = 0;
+    for (int t = unit; t < ntiles && !*abort_flag; t += units) {
+      int m, n;
+      tile_of(shape, t, &m, &n);
+      for (int kb = 0; kb < 2 * a.kblocks; ++kb, ++kc) {
+        const int s = kc % T::STAGES;
+        if (kc >= T::STAGES && !mbar_wait(&empty[s], ((kc / T::STAGES) - 1) & 1, abort_flag)) {
+          *abort_flag = 1; report_error(a.status, MOE_ERR_TIMEOUT, 60); break;
+        }
+        unsigned char* st = base + size_t(s) * T::STAGE;
+        const bool second = kb >= a.kblocks;
+        const int k0 = (second ? kb - a.kblocks : kb) * BK, row0 = m * T::BM + rank * 128;
+        if (rank == 0) mbar_arrive_expect_tx(&full[s], CG * (second ? D_STAGE : T::STAGE));
+        const uint32_t bar = CG == 1 ? smem_u32(&full[s]) : in_leader(&full[s]);
+        if (!second) {
+          load_operand<CG>(st, &tm_x, 0, row0, 128, k0, bar);
+          load_operand<CG>(st + kAStage, &tm_wgu, 0, n * 2 * NI + rank * T::BROWS, T::BROWS, k0, bar);
+        } else {
+          load_operand<CG>(st, &tm_dy, 0, row0, 128, k0, bar);
+          load_operand<CG>(st + kAStage, &tm_wd, 1, n * NI + rank * DROWS, DROWS, k0, bar);
+        }
+      }
+    }
+    // no copy and no release of a stage is under way when this SM leaves
+    for (int i = max(0, kc - T::STAGES); i < kc; ++i) {
+      const int s = i % T::STAGES;
+      bool ok = rank != 0 || mbar_wait(&full[s], (i / T::STAGES) & 1, nullptr);
+      ok = ok && (*abort_flag || mbar_wait(&empty[s], (i / T::STAGES) & 1, abort_flag));
+      if (!ok) report_error(a.status, MOE_ERR_TIMEOUT, 61);
+    }
+  } else if (warp == kGradEpi + 1 && rank == 0) {
+    int kc = 0, tc = 0;
+    bool ok = true;
+    for (int t = unit; t < ntiles && ok; t += units, ++tc) {
+      if (__any_sync(0xffffffffu, *abort_flag != 0)) break;
+      const int buf = tc & 1;
+      for (int ph = 0; ph < 2 && ok; ++ph) {
+        if (ph == 0 && tc >= 1)
+          ok = __all_sync(0xffffffffu, mbar_wait(gu_empty, (tc - 1) & 1, abort_flag));
+        if (ph == 1 && tc >= 2)
+          ok = __all_sync(0xffffffffu, mbar_wait(&dh_empty[buf], ((tc >> 1) - 1) & 1, abort_flag));
+        if (!ok) {
+          if (lane == 0) { *abort_flag = 1; report_error(a.status, MOE_ERR_TIMEOUT, 62); }
+          break;
+        }
+        tc_fence_after();
+        const uint32_t idesc = instr_desc(a.bf16, 0, ph, T::BM, ph ? NI : 2 * NI);
+        const uint32_t d = tmem + (ph ? uint32_t(2 * NI + buf * NI) : 0u);
+        for (int kb = 0; kb < a.kblocks; ++kb, ++kc) {
+          const int s = kc % T::STAGES;
+          ok = __all_sync(0xffffffffu, mbar_wait(&full[s], (kc / T::STAGES) & 1, abort_flag));
+          if (!ok) {
+            if (lane == 0) { *abort_flag = 1; report_error(a.status, MOE_ERR_TIMEOUT, 63); }
+            break;
+          }
+          tc_fence_after();
+          const uint32_t sa = smem_u32(base + size_t(s) * T::STAGE);
+          if (elect_one()) {
+            mma_stage<CG>(d, sa, sa + kAStage, 0, ph, idesc, kb == 0);
+            commit<CG>(&empty[s]);
+            if (kb == a.kblocks - 1) commit<CG>(ph ? &dh_full[buf] : gu_full);
+          }
+          __syncwarp();
+        }
+      }
+    }
+  } else if (warp < kGradEpi) {
+    const int q = warp & 3, part = warp >> 2;
+    constexpr int PI = NI / 4;                    // hidden elements of this thread
+    int tc = 0;
+    for (int t = unit; t < ntiles; t += units, ++tc) {
+      int m, n;
+      tile_of(shape, t, &m, &n);
+      const int buf = tc & 1;
+      const int row = m * T::BM + rank * 128 + q * 32 + lane;
+      const int i0 = n * NI + part * PI;
+      const uint32_t tq = tmem + (uint32_t(q * 32) << 16);
+      bool ok = !*abort_flag && mbar_wait(gu_full, tc & 1, abort_flag);
+      if (!__all_sync(0xffffffffu, ok)) {
+        if (!*abort_flag) { *abort_flag = 1; report_error(a.status, MOE_ERR_TIMEOUT, 65); }
+        break;
+      }
+      tc_fence_after();
+      float fg[PI], fu[PI];
+#pragma unroll
+      for (int c = 0; c < PI; c += 8) {
+        uint32_t v[16];
+        tmem_ld16(tq + uint32_t(2 * (part * PI + c)), v);
+        float hv[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float g = __uint_as_float(v[2 * j]), u = __uint_as_float(v[2 * j + 1]);
+          const float s = sigmoid(g), act = g * s;
+          hv[j] = act * u;
+          fu[c + j] = act;
+          fg[c + j] = u * fmaf(act, 1.f - s, s);
+        }
+        if (a.h && row < a.T) store_row<8>(a.h + size_t(row) * a.I, i0 + c, a.I, hv, a.bf16);
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) arrive_leader<CG>(gu_empty);
+      ok = !*abort_flag && mbar_wait(&dh_full[buf], (tc >> 1) & 1, abort_flag);
+      if (!__all_sync(0xffffffffu, ok)) {
+        if (!*abort_flag) { *abort_flag = 1; report_error(a.status, MOE_ERR_TIMEOUT, 66); }
+        break;
+      }
+      tc_fence_after();
+#pragma unroll
+      for (int c = 0; c < PI; c += 16) {
+        uint32_t v[16];
+        tmem_ld16(tq + uint32_t(2 * NI + buf * NI + part * PI + c), v);
+        if (row < a.T) {
+#pragma unroll
+          for (int e = 0; e < 16; e += 4) {
+            float d[8];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float dh = __uint_as_float(v[e + j]);
+              d[2 * j] = dh * fg[c + e + j];
+              d[2 * j + 1] = dh * fu[c + e + j];
+            }
+            store_row<8>(a.dgu + size_t(row) * 2 * a.I, 2 * (i0 + c + e), 2 * a.I, d, a.bf16);
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) arrive_leader<CG>(&dh_empty[buf]);
+    }
+  }
+
+  __syncwarp();
+  tc_fence_before();
+  if (CG == 1) __syncthreads();
+  else cluster_sync();
+  if (warp == kGradEpi + 1) {
+    tc_fence_after();
+    tmem_free<CG>(tmem, kCols);
+  }
+}
+
+// ------------------------------------------------------------------ host
+// Tensor map of one operand: [rows][cols] row-major.  Along the reduction
+// (mn = 0): boxes of 64 columns x box_rows rows; along its rows (mn = 1, the
+// rows of the operand are the matrix's columns): 64 columns x 64 rows.
+bool operand_map(CUtensorMap* m, int bf16, const void* p, int rows, int cols, int mn, int box_rows) {
+  return make_map(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, p, uint64_t(cols),
+                  uint64_t(rows), BK, mn ? 64 : uint32_t(box_rows), CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+template <typename... KArgs, typename... Args>
+cudaError_t launch_cluster(void (*kernel)(KArgs...), int cg, int grid, int threads, size_t smem, cudaStream_t s,
+                           const Args&... args) {
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = unsigned(cg);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cg > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+// One operand pair of a launch: matrices as stored.
+struct Operands {
+  const void* a; int a_rows, a_cols;
+  const void* b; int b_rows, b_cols;
+};
+
+int ceil_div(int a, int b) { return (a + b - 1) / b; }
+
+// The wide tile (256 x 256 on two SMs) or the narrow one (128 x 64 on one):
+// the one whose busiest SM finishes first.  A 64-deep step takes about 512
+// cycles on the wide tile (its products) and 260 on the narrow one (its
+// operands' way through L2).
+bool wide_tiles(const Problem* p, int n, int num_sms) {
+  double wide = 0, narrow = 0, wmax = 0, nmax = 0;
+  for (int i = 0; i < n; ++i) {
+    const double w = double(ceil_div(p[i].M, 256)) * ceil_div(p[i].N, 256);
+    const double s = double(ceil_div(p[i].M, 128)) * ceil_div(p[i].N, 64);
+    wide += w * p[i].kblocks;
+    narrow += s * p[i].kblocks;
+    if (p[i].kblocks > wmax) wmax = nmax = p[i].kblocks;
+  }
+  wide = wide / (num_sms / 2);
+  narrow = narrow / num_sms;
+  return (wide > wmax ? wide : wmax) * 512 <= (narrow > nmax ? narrow : nmax) * 260;
+}
+
+template <int CG, int BN, int EPI>
+cudaError_t launch_gemm(GemmArgs& a, const Operands* op, int num_sms, cudaStream_t s) {
+  using T = Tile<CG, BN>;
+  GemmMaps maps;
+  a.ntiles = 0;
+  for (int i = 0; i < a.n; ++i) {
+    Problem& p = a.p[i];
+    p.tiles_m = ceil_div(p.M, T::BM);
+    p.tiles_n = ceil_div(p.N, BN);
+    p.tile0 = a.ntiles;
+    a.ntiles += p.tiles_m * p.tiles_n;
+    if (!operand_map(&maps.a[i], a.bf16, op[i].a, op[i].a_rows, op[i].a_cols, p.a_mn, 128) ||
+        !operand_map(&maps.b[i], a.bf16, op[i].b, op[i].b_rows, op[i].b_cols, p.b_mn, T::BROWS))
+      return cudaErrorInvalidValue;
+  }
+  for (int i = a.n; i < 3; ++i) { maps.a[i] = maps.a[0]; maps.b[i] = maps.b[0]; }
+  const int units = min(num_sms / CG, a.ntiles);
+  return launch_cluster(ffn_gemm_kernel<CG, BN, EPI>, CG, units * CG, kGemmThreads, T::SMEM, s, a, maps);
+}
+
+template <int EPI>
+cudaError_t launch_products(GemmArgs& a, const Operands* op, int num_sms, cudaStream_t s) {
+  return wide_tiles(a.p, a.n, num_sms) ? launch_gemm<2, 256, EPI>(a, op, num_sms, s)
+                                       : launch_gemm<1, 64, EPI>(a, op, num_sms, s);
+}
+
+template <int CG, int NI>
+cudaError_t launch_grad(GradArgs& a, const FfnCall& c, int num_sms, cudaStream_t s) {
+  using T = Tile<CG, 2 * NI>;
+  CUtensorMap x, wgu, dy, wd;
+  if (!operand_map(&x, a.bf16, c.x, c.T, c.H, 0, 128) ||
+      !operand_map(&wgu, a.bf16, c.w_gate_up, 2 * c.I, c.H, 0, T::BROWS) ||
+      !operand_map(&dy, a.bf16, c.dy, c.T, c.H, 0, 128) || !operand_map(&wd, a.bf16, c.w_down, c.H, c.I, 1, 64))
+    return cudaErrorInvalidValue;
+  a.tiles_m = ceil_div(c.T, T::BM);
+  a.tiles_n = ceil_div(c.I, NI);
+  const int units = min(num_sms / CG, a.tiles_m * a.tiles_n);
+  return launch_cluster(ffn_grad_kernel<CG, NI>, CG, units * CG, kGradThreads, T::SMEM, s, a, x, wgu, dy, wd);
+}
+
+struct FfnLayout {
+  size_t status, h, dgu, total;
+};
+FfnLayout ffn_layout(int H, int I, int T, bool backward) {
+  (void)H;
+  FfnLayout l{};
+  l.status = 0;
+  l.h = 256;
+  l.dgu = l.h + align256(size_t(T) * I * 2);
+  l.total = l.dgu + (backward ? align256(size_t(T) * 2 * I * 2) : 0);
+  return l;
+}
+
+Problem problem(int M, int N, int K, int a_mn, int b_mn, void* out) {
+  Problem p{};
+  p.M = M; p.N = N; p.kblocks = ceil_div(K, BK); p.a_mn = a_mn; p.b_mn = b_mn; p.out = out; p.ld = N;
+  return p;
+}
+
+}  // namespace
+
+size_t ffn_workspace_bytes(int H, int I, int T, bool backward) { return ffn_layout(H, I, T, backward).total; }
+
+cudaError_t launch_ffn_forward(const FfnCall& c, int num_sms, cudaStream_t s) {
+  char* ws = static_cast<char*>(c.ws);
+  const FfnLayout l = ffn_layout(c.H, c.I, c.T, false);
+  void* h = ws + l.h;
+  GemmArgs a{};
+  a.bf16 = c.type == MOE_BF16;
+  a.status = reinterpret_cast<int*>(ws + l.status);
+  a.n = 1;
+  a.reset = 1;
+  a.p[0] = problem(c.T, 2 * c.I, c.H, 0, 0, h);
+  a.p[0].ld = c.I;
+  const Operands gu{c.x, c.T, c.H, c.w_gate_up, 2 * c.I, c.H};
+  cudaError_t e = launch_products<EPI_GATED>(a, &gu, num_sms, s);
+  if (e != cudaSuccess) return e;
+  a.reset = 0;
+  a.p[0] = problem(c.T, c.H, c.I, 0, 0, c.y);
+  const Operands dn{h, c.T, c.I, c.w_down, c.H, c.I};
+  return launch_products<EPI_STORE>(a, &dn, num_sms, s);
+}
+
+cudaError_t launch_ffn_backward(const FfnCall& c, int num_sms, cudaStream_t s) {
+  char* ws = static_cast<char*>(c.ws);
+  const FfnLayout l = ffn_layout(c.H, c.I, c.T, true);
+  void* h = ws + l.h;
+  void* dgu = ws + l.dgu;
+  GradArgs g{};
+  g.T = c.T; g.H = c.H; g.I = c.I;
+  g.kblocks = ceil_div(c.H, BK);
+  g.bf16 = c.type == MOE_BF16;
+  g.reset = 1;
+  g.h = c.dw_down ? static_cast<uint16_t*>(h) : nullptr;
+  g.dgu = static_cast<uint16_t*>(dgu);
+  g.status = reinterpret_cast<int*>(ws + l.status);
+  const Problem gp = problem(c.T, 2 * c.I, c.H, 0, 0, nullptr);
+  cudaError_t e = wide_tiles(&gp, 1, num_sms) ? launch_grad<2, 128>(g, c, num_sms, s) : launch_grad<1, 64>(g, c, num_sms, s);
+  if (e != cudaSuccess) return e;
+
+  GemmArgs a{};
+  a.bf16 = g.bf16;
+  a.status = g.status;
+  Operands op[3];
+  Problem p[3];
+  int n = 0;
+  if (c.dx) {
+    op[n] = {dgu, c.T, 2 * c.I, c.w_gate_up, 2 * c.I, c.H};
+    p[n++] = problem(c.T, c.H, 2 * c.I, 0, 1, c.dx);
+  }
+  if (c.dw_gate_up) {
+    op[n] = {dgu, c.T, 2 * c.I, c.x, c.T, c.H};
+    p[n++] = problem(2 * c.I, c.H, c.T, 1, 1, c.dw_gate_up);
+  }
+  if (c.dw_down) {
+    op[n] = {c.dy, c.T, c.H, h, c.T, c.I};
+    p[n++] = problem(c.H, c.I, c.T, 1, 1, c.dw_down);
+  }
+  if (n == 0) return cudaSuccess;
+  // the deepest products first: the last tiles to finish are short ones
+  int order[3] = {0, 1, 2};
+  for (int i = 1; i < n; ++i)
+    for (int j = i; j > 0 && p[order[j]].kblocks > p[order[j - 1]].kblocks; --j) {
+      const int o = order[j];
+      order[j] = order[j - 1];
+      order[j - 1] = o;
+    }
+  Operands sorted[3];
+  for (int i = 0; i < n; ++i) {
+    a.p[i] = p[order[i]];
+    sorted[i] = op[order[i]];
+  }
+  a.n = n;
+  return launch_products<EPI_STORE>(a, sorted, num_sms, s);
+}
+
+}  // namespace moe
