@@ -248,8 +248,8 @@ typedef enum moe_type { MOE_BF16 = 0, MOE_FP16 = 1, MOE_FP32 = 2 } moe_type;
  * T (meant for decode batches: T > 32 is cut into slices that each read the
  * weights); cols a multiple of the block, at most 32768.  Products and sums
  * are fp32, rounded once to y_type; the activations are taken exactly but for
- * elements smaller than 2^-31 of their row's largest magnitude, which are off
- * by at most 2^-35 of it.  A row of x that holds an infinity or a NaN gives a
+ * elements smaller than 2^-27 of their row's largest magnitude, which are off
+ * by at most 2^-38 of it.  A row of x that holds an infinity or a NaN gives a
  * row of NaN.  The call reads the weights before it waits for a kernel ahead
  * of it that lets its dependents launch early; none in this library writes
  * weights. */

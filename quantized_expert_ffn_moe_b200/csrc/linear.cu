@@ -1,11 +1,11 @@
 // Products of few token rows with a packed 4-bit matrix: a plain linear layer
 // and the gate/up half of a gated feed-forward block.
 //
-//   z[t][n] = rs_n * sum_b s_{n,b} * sum_{k in block b} (c_{n,k} - off) x[t][k]
+//   z[t][n] = rs_n * sum_b s_{n,b} * sum_{k in block b} q_{n,k} x[t][k]
 //   linear: y[t][n] = z[t][n] (+ bias[n]);   gated: h[t][i] = silu(z[t][2i]) * z[t][2i+1]
 //
-// (c the stored code, off = 8 or 7.5, s the block's scale, rs the row scale of
-// the fp8 format.)  Bound by the packed bytes, n * k / 2 plus the scales.
+// (q the code's level, s the block's scale, rs the row scale of the fp8
+// format.)  Bound by the packed bytes, n * k / 2 plus the scales.
 //
 // A warp multiplies 16 rows at a time with the warp-level tensor instruction
 // m16n8k16 (fp16 operands, fp32 accumulation), rows as M and up to 8 tokens as
@@ -14,25 +14,23 @@
 // token.  The instruction issues every 2 cycles per SM (measured); the HBM
 // rate brings 16 rows x 16 codes every 5.5 cycles, so up to two groups of 8
 // tokens run below the memory bound and dequantising is what must be cheap:
-//  * A code is never converted.  Its bits, masked in place, are an fp16
-//    subnormal: c * 2^-24 (mask 0x000f000f) or 16 c * 2^-24 (0x00f000f0), and
-//    the tensor core takes subnormals exactly.  Eight codes cost four masks
-//    and one shift.  The factor 16 is divided out of the activations of the
-//    odd elements (a power of two, exact).
-//  * The offset is not subtracted from the codes: the accumulator of a block
-//    starts at -off * 2^-24 * sum_{k in b} x[t][k], computed once per call.
-//  * The k order inside a block is free as long as both operands share it:
-//    lane t of a row's quad takes the block's t-th 32-bit word, as stored.
+// eight codes become exact fp16 integers with four masks, one shift and four
+// half2 operations.  (Fed as they are, as fp16 subnormals, with the offset
+// taken off through the accumulator, they cost half of that, but the sums
+// then carry the offset's magnitude: 4 to 8 times the rounding error.)
+// The k order inside a block is free as long as both operands share it: lane
+// t of a row's quad takes the block's t-th 32-bit word, as stored.
+//
 // Activations become fp16 after the power of two that brings the row's largest
-// magnitude into [2^13, 2^14): exact for every element within 2^-31 of that
-// largest one, off by at most 2^-35 of it below (fp32 sums lose more).  A row
+// magnitude into [2^13, 2^14): exact for every element within 2^-27 of that
+// largest one, off by at most 2^-38 of it below (fp32 sums lose more).  A row
 // with an infinity or a NaN gives NaN in all its outputs.
 //
-// Each warp streams its own 16 rows x 128 columns stages through a private
-// ring of asynchronous copies (no block-wide barrier in the stream); the warps
-// of a group split the columns of a row tile, so that even 2048 x 2048 spreads
-// over 128 SMs, and join their fp32 sums through shared memory in a fixed
-// order: the same inputs give the same bits.
+// Each warp streams its own stages of 16 rows x 128 or 256 columns through a
+// private ring of asynchronous copies (no block-wide barrier in the stream);
+// the warps of a group split the columns of a row tile, so that even 2048 x
+// 2048 spreads over 128 SMs, and join their fp32 sums through shared memory in
+// a fixed order: the same inputs give the same bits.
 #include "dense_internal.cuh"
 
 namespace moe {
@@ -41,15 +39,28 @@ namespace {
 
 constexpr int kWarps = 16;
 constexpr int kThreads = kWarps * 32;
-constexpr int kStages = 4;
-constexpr int kChunk = 128;                                 // columns of a stage
-constexpr int kCodeBytes = 16 * kChunk / 2;                 // 1 KB of codes
-constexpr int kStageBytes = kCodeBytes + 128;               // + up to 16 x 4 fp16 scales
-constexpr int kRingBytes = kWarps * kStages * kStageBytes;
 constexpr size_t kMaxSmem = 232448;
 
-// scale formats: fp16 per 32, fp16 per 128, E4M3 per 32 under a row scale
-enum { F_H32 = 0, F_H128 = 1, F_E32 = 2 };
+// scale formats: fp16 per 32, fp16 per 128, E4M3 per 32 under a row scale; the
+// fp16 ones with integer or half-integer levels
+enum { F_H32 = 0, F_H128 = 1, F_E32 = 2, F_H32_HALF = 3, F_H128_HALF = 4 };
+template <int FMT>
+struct Format {
+  static constexpr bool HALF = FMT == F_H32_HALF || FMT == F_H128_HALF;
+  static constexpr bool G128 = FMT == F_H128 || FMT == F_H128_HALF;
+  static constexpr int SB = FMT == F_E32 ? 1 : 2;            // bytes of a scale
+};
+// A stage: 16 rows x CB blocks of 32 columns, codes then scales (up to CB fp16
+// a row), in a ring of ST slots per warp.  8 blocks halve the per-stage work;
+// 4 leave room for more activations.
+template <int CB>
+struct Stage {
+  static constexpr int ROW = CB * 16;
+  static constexpr int CODES = 16 * ROW;
+  static constexpr int BYTES = CODES + 32 * CB;
+  static constexpr int ST = CB == 8 ? 3 : 4;
+  static constexpr int RING = kWarps * ST * BYTES;
+};
 
 struct LinearArgs {
   const uint8_t* codes;
@@ -60,11 +71,11 @@ struct LinearArgs {
   void* y;
   int N, K, T;          // matrix rows, columns, token rows
   int nb;               // 32-element blocks of a row
-  int chunks;           // 128-column stages of a row
+  int spr;              // scales of a row
+  int chunks;           // stages of a row
   int KG, groups;       // warps splitting a row tile's columns; row tiles in flight per CTA
   int ny, tt;           // token slices, tokens of a slice
-  int x_type, y_type, gated, aligned;
-  float off;
+  int x_type, y_type, gated;
 };
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
@@ -78,53 +89,106 @@ __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commi
 template <int N>
 __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
-__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                         uint32_t b0, uint32_t b1) {
-  asm(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Scales of a stage's four blocks of one row as floats, from the row's slot of
-// 8 (fp16), 4 (E4M3) or 2 bytes (one fp16 for all four).
-template <int FMT>
-__device__ __forceinline__ void stage_scales(const unsigned char* sc, int row, float (&s)[4]) {
-  if (FMT == F_H32) {
-    const uint2 v = *reinterpret_cast<const uint2*>(sc + row * 8);
-    const float2 a = __half22float2(u32_as_h2(v.x)), b = __half22float2(u32_as_h2(v.y));
-    s[0] = a.x; s[1] = a.y; s[2] = b.x; s[3] = b.y;
-  } else if (FMT == F_E32) {
-    const uint32_t v = *reinterpret_cast<const uint32_t*>(sc + row * 4);
-    uint32_t lo, hi;
-    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
-        : "=r"(lo), "=r"(hi) : "r"(v));
-    const float2 a = __half22float2(u32_as_h2(lo)), b = __half22float2(u32_as_h2(hi));
-    s[0] = a.x; s[1] = a.y; s[2] = b.x; s[3] = b.y;
+// Eight codes as exact fp16 pairs (e_j, e_{j+4}), j = 0..3.  Integer levels:
+// c - 8; half-integer levels: 2 c - 15, twice the level (halved at the end).
+// A 16-bit lane 0x6400 | m is 1024 + m.
+template <bool HALF>
+__device__ __forceinline__ void levels(uint32_t w, uint32_t (&q)[4]) {
+  if (!HALF) {
+    __half2 h[4];
+    decode_q4x8(w, h);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) q[j] = h2_as_u32(h[j]);
   } else {
-    const float v = __half2float(*reinterpret_cast<const __half*>(sc + row * 2));
-    s[0] = v; s[1] = v; s[2] = v; s[3] = v;
+    const uint32_t MAGIC = 0x64006400u;
+    const __half2 sub = u32_as_h2(0x640F640Fu);                                    // 1039 = 1024 + 15
+    const __half2 mul = u32_as_h2(0x30003000u), add = u32_as_h2(0xD878D878u);      // 1/8, -143 = -(128 + 15)
+    q[0] = h2_as_u32(__hsub2(u32_as_h2(lop_and_or(w << 1, 0x001E001Eu, MAGIC)), sub));
+    q[1] = h2_as_u32(__hfma2(u32_as_h2(lop_and_or(w, 0x00F000F0u, MAGIC)), mul, add));
+    q[2] = h2_as_u32(__hsub2(u32_as_h2(lop_and_or(w >> 7, 0x001E001Eu, MAGIC)), sub));
+    q[3] = h2_as_u32(__hfma2(u32_as_h2(lop_and_or(w >> 8, 0x00F000F0u, MAGIC)), mul, add));
   }
 }
 
-// Shared memory: ring | x [nb][tt][4] 16-byte words | init [nb][8 NT] floats |
-// partial sums [groups KG][16][8 NT] floats | inv [8 NT] floats | row maxima
-// [tt][16] u32.
-__host__ __device__ inline size_t linear_smem(int nb, int tt, int nt) {
-  return size_t(kRingBytes) + size_t(nb) * tt * 64 + size_t(nb) * nt * 32 + size_t(kWarps) * 16 * 8 * nt * 4 +
-         size_t(nt) * 32 + size_t(tt) * 64;
+// Scales of a row's blocks in a stage as floats (one for all with groups of
+// 128 and CB = 4, two with CB = 8).
+template <int FMT, int CB>
+__device__ __forceinline__ void stage_scales(const unsigned char* sc, int row, float (&s)[CB]) {
+  if (Format<FMT>::G128) {
+    const __half* p = reinterpret_cast<const __half*>(sc) + row * (CB / 4);
+    const float a = __half2float(p[0]), b = CB == 8 ? __half2float(p[1]) : a;
+#pragma unroll
+    for (int i = 0; i < CB; ++i) s[i] = i < 4 ? a : b;
+  } else {
+    uint32_t w[CB / 2];
+    if (FMT == F_E32) {
+#pragma unroll
+      for (int i = 0; i < CB / 4; ++i) {
+        const uint32_t v = *reinterpret_cast<const uint32_t*>(sc + row * CB + 4 * i);
+        asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\t"
+            "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+            : "=r"(w[2 * i]), "=r"(w[2 * i + 1]) : "r"(v));
+      }
+    } else if (CB == 8) {
+      const uint4 v = *reinterpret_cast<const uint4*>(sc + row * 16);
+      w[0] = v.x; w[1] = v.y; w[CB / 2 - 2] = v.z; w[CB / 2 - 1] = v.w;
+    } else {
+      const uint2 v = *reinterpret_cast<const uint2*>(sc + row * 8);
+      w[0] = v.x; w[1] = v.y;
+    }
+#pragma unroll
+    for (int i = 0; i < CB / 2; ++i) {
+      const float2 f = __half22float2(u32_as_h2(w[i]));
+      s[2 * i] = f.x;
+      s[2 * i + 1] = f.y;
+    }
+  }
 }
 
-template <int NT, int FMT>
+// Shared memory: ring | x [nb][tt][4] 16-byte words | partial sums [groups
+// KG][16][8 NT] floats | inv [8 NT] floats | row maxima [tt][16] u32.
+inline size_t linear_smem(int ring, int nb, int tt, int nt) {
+  return size_t(ring) + size_t(nb) * tt * 64 + size_t(kWarps) * 16 * 8 * nt * 4 + size_t(nt) * 32 + size_t(tt) * 64;
+}
+
+// Eight activations as fp16 pairs (j, j + 4), the order of `levels`.
+__device__ __forceinline__ uint4 pack_activations(const uint4& v, bool bf, float mul) {
+  const uint32_t q[4] = {v.x, v.y, v.z, v.w};
+  float f[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (bf) {
+      f[2 * i] = __uint_as_float(q[i] << 16);
+      f[2 * i + 1] = __uint_as_float(q[i] & 0xffff0000u);
+    } else {
+      const float2 h = __half22float2(u32_as_h2(q[i]));
+      f[2 * i] = h.x;
+      f[2 * i + 1] = h.y;
+    }
+  }
+  uint32_t o[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) o[j] = h2_as_u32(__floats2half2_rn(f[j] * mul, f[j + 4] * mul));
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+template <int NT, int FMT, int CB>
 __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const LinearArgs a) {
+  using F = Format<FMT>;
+  using S = Stage<CB>;
   extern __shared__ __align__(128) unsigned char lsm[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
   const int nb = a.nb, tt = a.tt;
   constexpr int TP = 8 * NT;
-  unsigned char* sx = lsm + kRingBytes;
-  float* sinit = reinterpret_cast<float*>(sx + size_t(nb) * tt * 64);
-  float* spart = sinit + size_t(nb) * TP;
+  unsigned char* sx = lsm + S::RING;
+  float* spart = reinterpret_cast<float*>(sx + size_t(nb) * tt * 64);
   float* sinv = spart + kWarps * 16 * TP;
   uint32_t* smax = reinterpret_cast<uint32_t*>(sinv + TP);
 
@@ -134,110 +198,144 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const LinearArgs a)
   const int ntiles = (a.N + 15) >> 4;
   const int grp = warp / a.KG, kw = warp - grp * a.KG;
   const int first = cta * a.groups + grp, step = ctas * a.groups;
-  const bool active = grp < a.groups;
-  const int my_chunks = active && kw < a.chunks ? (a.chunks - kw + a.KG - 1) / a.KG : 0;
-  const int my_tiles = active && first < ntiles ? (ntiles - first + step - 1) / step : 0;
+  const int my_chunks = grp < a.groups ? (a.chunks - kw + a.KG - 1) / a.KG : 0;
+  const int my_tiles = grp < a.groups && first < ntiles ? (ntiles - first + step - 1) / step : 0;
   const int total = my_tiles * my_chunks;
 
-  unsigned char* ring = lsm + warp * (kStages * kStageBytes);
-  const size_t row_bytes = size_t(a.K) >> 1;
-  constexpr int SPC = FMT == F_H128 ? 1 : 4;              // scales of a row in a stage
-  constexpr int SB = FMT == F_E32 ? 1 : 2;                // bytes of a scale
-  const int spr = FMT == F_H128 ? a.chunks : nb;          // scales of a row
-  // scales that cannot be copied asynchronously (rows off a 4- or 8-byte
-  // boundary, or one fp16 per stage) pass through registers: loaded with
+  // ------------------------------------------------------ weight stream
+  // This lane copies CB / 4 x 2 16-byte pieces of a stage's codes: piece
+  // `ch` of the rows r0 + i * RS, swizzled so that the words of eight rows
+  // fall into different banks.
+  unsigned char* ring = lsm + warp * (S::ST * S::BYTES);
+  const uint32_t ring_s = smem_u32(ring);
+  constexpr int RS = 32 / CB;                             // rows covered by one warp-wide copy
+  const int r0 = lane / CB, ch = lane % CB;
+  const int row_bytes = a.K >> 1;
+  constexpr int SPC = F::G128 ? CB / 4 : CB;              // scales of a row in a stage
+  // scales that cannot be copied asynchronously (rows off the copy's
+  // alignment, or one fp16 per stage) pass through registers: loaded with
   // their stage's codes, stored to its slot when the next stage is issued
+  constexpr bool kMayCopy = SPC * F::SB >= 4;
+  const bool direct = kMayCopy && a.spr % SPC == 0;
   constexpr int PEND = (16 * SPC + 31) / 32;
   uint16_t pend[PEND];
   int pend_slot = -1;
-  const bool direct = FMT != F_H128 && a.aligned;
-
-  int it_tile = first, it_chunk = kw, issued = 0;
   auto flush_pending = [&]() {
     if (pend_slot < 0) return;
-    unsigned char* sc = ring + pend_slot * kStageBytes + kCodeBytes;
+    unsigned char* sc = ring + pend_slot * S::BYTES + S::CODES;
 #pragma unroll
     for (int i = 0; i < PEND; ++i) {
       const int e = i * 32 + lane;
       if (e < 16 * SPC) {
-        if (SB == 2) *reinterpret_cast<uint16_t*>(sc + e * 2) = pend[i];
+        if (F::SB == 2) *reinterpret_cast<uint16_t*>(sc + e * 2) = pend[i];
         else sc[e] = uint8_t(pend[i]);
       }
     }
     pend_slot = -1;
   };
+  const uint8_t* src = nullptr;      // this lane's piece of the next stage, row r0 of its tile
+  const uint8_t* ssrc = nullptr;     // (direct) the scales of row `lane` of that tile
+  int it_tile = first, it_chunk = 0, left = total, slot_i = 0;
+  bool ragged = false;               // the tile reaches past the last row
+  auto enter_tile = [&]() {
+    it_chunk = kw;
+    ragged = it_tile * 16 + 16 > a.N;
+    src = a.codes + size_t(it_tile * 16 + r0) * row_bytes + size_t(kw) * S::ROW + ch * 16;
+    ssrc = static_cast<const uint8_t*>(a.scales) +
+           (size_t(min(it_tile * 16 + (lane & 15), a.N - 1)) * a.spr + size_t(kw) * SPC) * F::SB;
+  };
+  if (left > 0) enter_tile();
   auto issue = [&]() {
     if (!direct) flush_pending();
-    if (issued < total) {
-      const int slot = issued % kStages;
-      const uint32_t dst = smem_u32(ring) + slot * kStageBytes;
-      const int row0 = it_tile * 16;
+    if (left > 0) {
+      const uint32_t dst = ring_s + slot_i * S::BYTES;
+      const bool in = it_chunk * CB + ch < nb;            // the last stage of a row may be short
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int r = i * 8 + (lane >> 2), ch = lane & 3;
-        if (it_chunk * 4 + ch < nb)
-          cp_async16(dst + r * 64 + ((ch ^ ((r >> 1) & 3)) << 4),
-                     a.codes + size_t(min(row0 + r, a.N - 1)) * row_bytes + size_t(it_chunk) * 64 + ch * 16);
+      for (int i = 0; i < CB / 2; ++i) {
+        const int r = r0 + i * RS;
+        int sr = i * RS;
+        if (ragged) sr = min(sr, a.N - 1 - it_tile * 16 - r0);       // rows past the end: the last one again
+        if (in)
+          cp_async16(dst + r * S::ROW + ((ch ^ (CB == 8 ? r & 7 : (r >> 1) & 3)) << 4), src + ptrdiff_t(sr) * row_bytes);
       }
       if (direct) {
-        if (lane < 16)
-          cp_async_small<4 * SB>(dst + kCodeBytes + lane * (4 * SB),
-                                 static_cast<const uint8_t*>(a.scales) +
-                                     (size_t(min(row0 + lane, a.N - 1)) * spr + size_t(it_chunk) * 4) * SB);
+        if (lane < 16) {
+          constexpr int B = kMayCopy ? SPC * F::SB : 4;
+          if (B == 16) cp_async16(dst + S::CODES + lane * 16, ssrc);
+          else cp_async_small<B == 16 ? 8 : B>(dst + S::CODES + lane * B, ssrc);
+        }
       } else {
 #pragma unroll
         for (int i = 0; i < PEND; ++i) {
-          const int e = i * 32 + lane, r = e / SPC, b = it_chunk * SPC + e % SPC;
+          const int e = i * 32 + lane, b = it_chunk * SPC + e % SPC;
           pend[i] = 0;
-          if (e < 16 * SPC && b < spr) {
-            const size_t at = size_t(min(row0 + r, a.N - 1)) * spr + b;
-            pend[i] = SB == 2 ? ld_stream2(static_cast<const uint16_t*>(a.scales) + at)
-                              : uint16_t(__ldg(static_cast<const uint8_t*>(a.scales) + at));
+          if (e < 16 * SPC && b < a.spr) {
+            const size_t at = size_t(min(it_tile * 16 + e / SPC, a.N - 1)) * a.spr + b;
+            pend[i] = F::SB == 2 ? ld_stream2(static_cast<const uint16_t*>(a.scales) + at)
+                                 : uint16_t(__ldg(static_cast<const uint8_t*>(a.scales) + at));
           }
         }
-        pend_slot = slot;
+        pend_slot = slot_i;
       }
-      ++issued;
+      --left;
+      slot_i = slot_i + 1 == S::ST ? 0 : slot_i + 1;
       it_chunk += a.KG;
-      if (it_chunk >= a.chunks) { it_chunk = kw; it_tile += step; }
+      src += a.KG * S::ROW;
+      ssrc += a.KG * SPC * F::SB;
+      if (it_chunk >= a.chunks) {
+        it_tile += step;
+        if (left > 0) enter_tile();
+      }
     }
     cp_async_commit();
   };
   // the weights do not depend on the previous kernel of the stream
 #pragma unroll
-  for (int s = 0; s < kStages - 1; ++s) issue();
+  for (int s = 0; s < S::ST - 1; ++s) issue();
 
   pdl_wait();
   pdl_launch_dependents();
 
   // ------------------------------------------------------ activations
   // A unit is (token, slice of its columns); with fewer tokens than warps a
-  // token's columns are split over several warps.
+  // token's columns are split over several warps.  A unit's words are held in
+  // registers between the maximum and the conversion when they fit there.
   {
+    constexpr int HOLD = 8;
     const int sl = nt >= kWarps ? 1 : kWarps / nt;         // slices of a token
     const int units = nt * sl;
     const int K8 = a.K >> 3;                               // 16-byte words of a token row
-    const int per = ((K8 + sl - 1) / sl + 3) & ~3;         // whole blocks per slice
+    const int per = (K8 + sl - 1) / sl;
+    const bool bf = a.x_type == MOE_BF16;
     const uint16_t* xb = static_cast<const uint16_t*>(a.x) + size_t(t0) * a.K;
+    const bool held = units <= kWarps && per <= HOLD * 32;
+    uint4 hold[HOLD];
+    auto word_max = [](uint32_t m, const uint4& v) {
+      const uint32_t q = __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu),
+                                  __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
+      return __vmaxu2(m, q);
+    };
     for (int u = warp; u < units; u += kWarps) {
-      const int n = u / sl, p = u % sl;
-      const uint4* src = reinterpret_cast<const uint4*>(xb + size_t(n) * a.K);
+      const int n = u / sl, p = u % sl, end = min(K8, (p + 1) * per);
+      const uint4* src8 = reinterpret_cast<const uint4*>(xb + size_t(n) * a.K);
       uint32_t m = 0;
-      for (int w = p * per + lane; w < min(K8, (p + 1) * per); w += 32) {
-        const uint4 v = __ldg(src + w);
-        const uint32_t q[4] = {v.x & 0x7fff7fffu, v.y & 0x7fff7fffu, v.z & 0x7fff7fffu, v.w & 0x7fff7fffu};
+      for (int w0 = p * per; w0 < end; w0 += HOLD * 32) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) m = max(m, max(q[i] & 0xffffu, q[i] >> 16));
+        for (int i = 0; i < HOLD; ++i) {
+          const int w = w0 + i * 32 + lane;
+          hold[i] = w < end ? __ldg(src8 + w) : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int i = 0; i < HOLD; ++i) m = word_max(m, hold[i]);
       }
-      m = __reduce_max_sync(0xffffffffu, m);
+      m = __reduce_max_sync(0xffffffffu, max(m & 0xffffu, m >> 16));
       if (lane == 0) smax[n * 16 + p] = m;
     }
     __syncthreads();
     for (int u = warp; u < units; u += kWarps) {
-      const int n = u / sl, p = u % sl;
-      uint32_t m = 0;
-      for (int i = 0; i < sl; ++i) m = max(m, smax[n * 16 + i]);
-      const bool bf = a.x_type == MOE_BF16;
+      const int n = u / sl, p = u % sl, end = min(K8, (p + 1) * per);
+      uint32_t m = lane < sl ? smax[n * 16 + lane] : 0u;
+      m = __reduce_max_sync(0xffffffffu, m);
       const bool finite = m < (bf ? 0x7f80u : 0x7c00u);
       const float top = bf ? __uint_as_float(m << 16) : __half2float(__ushort_as_half((unsigned short)m));
       int sh = 0;
@@ -247,48 +345,22 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const LinearArgs a)
         sh = min(max(14 - ex, -120), 120);
       }
       const float mul = ldexpf(1.f, sh);
-      if (p == 0 && lane == 0) sinv[n] = finite ? ldexpf(1.f, -sh) : __int_as_float(0x7fc00000);
-      const uint4* src = reinterpret_cast<const uint4*>(xb + size_t(n) * a.K);
-      const int end = min(K8, (p + 1) * per);
-      for (int w0 = p * per; w0 < end; w0 += 32) {
-        const int w = w0 + lane;
-        float f[8];
-        if (w < end) {
-          const uint4 v = __ldg(src + w);
-          const uint32_t q[4] = {v.x, v.y, v.z, v.w};
+      if (p == 0 && lane == 0) sinv[n] = finite ? ldexpf(F::HALF ? 0.5f : 1.f, -sh) : __int_as_float(0x7fc00000);
+      const uint4* src8 = reinterpret_cast<const uint4*>(xb + size_t(n) * a.K);
+      for (int w0 = p * per; w0 < end; w0 += HOLD * 32) {
+        if (!held) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            if (bf) {
-              f[2 * i] = __uint_as_float(q[i] << 16);
-              f[2 * i + 1] = __uint_as_float(q[i] & 0xffff0000u);
-            } else {
-              const float2 h = __half22float2(u32_as_h2(q[i]));
-              f[2 * i] = h.x;
-              f[2 * i + 1] = h.y;
-            }
+          for (int i = 0; i < HOLD; ++i) {
+            const int w = w0 + i * 32 + lane;
+            if (w < end) hold[i] = __ldg(src8 + w);
           }
-        } else {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) f[i] = 0.f;
         }
-        // element pairs (j, j + 4) as the masked code words hold them, the
-        // odd ones over 16; their sum from the rounded values
-        float sum = 0.f;
-        uint32_t o[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float m2 = (j & 1) ? mul * 0.0625f : mul;
-          const __half2 h = __floats2half2_rn(f[j] * m2, f[j + 4] * m2);
-          o[j] = h2_as_u32(h);
-          const float2 r = __half22float2(h);
-          sum += (r.x + r.y) * ((j & 1) ? 16.f : 1.f);
-        }
-        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-        if (w < end) {
-          const int b = w >> 2;
-          *reinterpret_cast<uint4*>(sx + (size_t(b) * tt + n) * 64 + (w & 3) * 16) = make_uint4(o[0], o[1], o[2], o[3]);
-          if ((w & 3) == 0) sinit[size_t(b) * TP + n] = -a.off * 5.9604644775390625e-8f * sum;
+        for (int i = 0; i < HOLD; ++i) {
+          const int w = w0 + i * 32 + lane;
+          if (w < end)
+            *reinterpret_cast<uint4*>(sx + (size_t(w >> 2) * tt + n) * 64 + (w & 3) * 16) =
+                pack_activations(hold[i], bf, mul);
         }
       }
     }
@@ -298,11 +370,10 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const LinearArgs a)
 
   // ------------------------------------------------------------ stream
   // this lane's words of the tokens 8 j + g (the last token's where there is
-  // none: those columns are never stored) and its pair of initial sums
+  // none: those columns are never stored)
   const unsigned char* xrow[NT];
 #pragma unroll
   for (int j = 0; j < NT; ++j) xrow[j] = sx + min(8 * j + g, nt - 1) * 64 + t * 16;
-  const float* init0 = sinit + 2 * t;
   const int xstep = tt * 64;
   float acc[NT][4];
 #pragma unroll
@@ -310,45 +381,55 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const LinearArgs a)
 #pragma unroll
     for (int i = 0; i < 4; ++i) acc[j][i] = 0.f;
 
-  int tile = first, chunk = kw;
+  int tile = first, chunk = kw, slot = 0;
   bool first_tile = true;
   for (int it = 0; it < total; ++it) {
     __syncwarp();                     // every lane is done with the slot that is filled next
     issue();
-    cp_async_wait<kStages - 1>();
+    cp_async_wait<S::ST - 1>();
     __syncwarp();
-    const unsigned char* st = ring + (it % kStages) * kStageBytes;
-    float s0[4], s1[4];
-    stage_scales<FMT>(st + kCodeBytes, g, s0);
-    stage_scales<FMT>(st + kCodeBytes, g + 8, s1);
-    const int nblk = min(4, nb - chunk * 4);
-    const unsigned char* code0 = st + g * 64 + t * 4;
-    const int sw = (g >> 1) & 3;                          // rows g and g + 8 share the swizzle
-    auto block = [&](int b) {
-      const uint32_t w0 = *reinterpret_cast<const uint32_t*>(code0 + ((b ^ sw) << 4));
-      const uint32_t w1 = *reinterpret_cast<const uint32_t*>(code0 + 512 + ((b ^ sw) << 4));
-      const uint32_t v0 = w0 >> 8, v1 = w1 >> 8;
-      const int bb = chunk * 4 + b;
+    const unsigned char* st = ring + slot * S::BYTES;
+    slot = slot + 1 == S::ST ? 0 : slot + 1;
+    float s0[CB], s1[CB];
+    stage_scales<FMT, CB>(st + S::CODES, g, s0);
+    stage_scales<FMT, CB>(st + S::CODES, g + 8, s1);
+    const int nblk = min(CB, nb - chunk * CB);
+    const unsigned char* code0 = st + g * S::ROW + t * 4;
+    const int sw = CB == 8 ? g : (g >> 1) & 3;            // rows g and g + 8 share the swizzle
+    const unsigned char* xc[NT];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) xc[j] = xrow[j] + chunk * CB * xstep;
+    float d[NT][4];
+    // fold: the sums so far take the scale of block b
+    auto block = [&](int b, bool start, bool fold) {
+      uint32_t q0[4], q1[4];
+      levels<F::HALF>(*reinterpret_cast<const uint32_t*>(code0 + ((b ^ sw) << 4)), q0);
+      levels<F::HALF>(*reinterpret_cast<const uint32_t*>(code0 + 8 * S::ROW + ((b ^ sw) << 4)), q1);
+      const uint32_t lo[4] = {q0[0], q1[0], q0[1], q1[1]}, hi[4] = {q0[2], q1[2], q0[3], q1[3]};
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
-        const uint4 xv = *reinterpret_cast<const uint4*>(xrow[j] + bb * xstep);
-        const float2 iv = *reinterpret_cast<const float2*>(init0 + bb * TP + 8 * j);
-        float d[4] = {iv.x, iv.y, iv.x, iv.y};
-        mma16816(d, w0 & 0x000f000fu, w1 & 0x000f000fu, w0 & 0x00f000f0u, w1 & 0x00f000f0u, xv.x, xv.y);
-        mma16816(d, v0 & 0x000f000fu, v1 & 0x000f000fu, v0 & 0x00f000f0u, v1 & 0x00f000f0u, xv.z, xv.w);
-        acc[j][0] = fmaf(s0[b], d[0], acc[j][0]);
-        acc[j][1] = fmaf(s0[b], d[1], acc[j][1]);
-        acc[j][2] = fmaf(s1[b], d[2], acc[j][2]);
-        acc[j][3] = fmaf(s1[b], d[3], acc[j][3]);
+        const uint4 xv = *reinterpret_cast<const uint4*>(xc[j] + b * xstep);
+        if (start) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) d[j][i] = 0.f;
+        }
+        mma16816(d[j], lo, xv.x, xv.y);
+        mma16816(d[j], hi, xv.z, xv.w);
+        if (fold) {
+          acc[j][0] = fmaf(s0[b], d[j][0], acc[j][0]);
+          acc[j][1] = fmaf(s0[b], d[j][1], acc[j][1]);
+          acc[j][2] = fmaf(s1[b], d[j][2], acc[j][2]);
+          acc[j][3] = fmaf(s1[b], d[j][3], acc[j][3]);
+        }
       }
     };
-    if (nblk == 4) {
+    if (nblk == CB) {
 #pragma unroll
-      for (int b = 0; b < 4; ++b) block(b);
+      for (int b = 0; b < CB; ++b) block(b, !F::G128 || (b & 3) == 0, !F::G128 || (b & 3) == 3);
     } else {
 #pragma unroll
-      for (int b = 0; b < 3; ++b)
-        if (b < nblk) block(b);
+      for (int b = 0; b < CB - 1; ++b)
+        if (b < nblk) block(b, !F::G128 || (b & 3) == 0, !F::G128 || (b & 3) == 3);
     }
     chunk += a.KG;
     if (chunk < a.chunks) continue;
@@ -373,9 +454,11 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const LinearArgs a)
     group_sync();
     const int row0 = tile * 16, tid = kw * 32 + lane;
     auto sum_of = [&](int row, int n) {
+      const float* p = gp + row * TP + n;
       float v = 0.f;
-      for (int w = 0; w < a.KG; ++w) v += gp[(w * 16 + row) * TP + n];
-      v = v * 16777216.f * sinv[n];
+#pragma unroll 4
+      for (int w = 0; w < a.KG; ++w) v += p[w * 16 * TP];
+      v *= sinv[n];
       if (FMT == F_E32) v *= __ldg(a.row_scales + row0 + row);
       return v;
     };
@@ -401,12 +484,33 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const LinearArgs a)
   cp_async_wait<0>();
 }
 
-template <int FMT>
+template <int FMT, int CB>
 cudaError_t launch_fmt(const LinearArgs& a, int nt, int grid, size_t smem, cudaStream_t s) {
-  auto kern = nt == 1 ? linear_kernel<1, FMT> : nt == 2 ? linear_kernel<2, FMT> : linear_kernel<4, FMT>;
+  auto kern = nt == 1 ? linear_kernel<1, FMT, CB> : nt == 2 ? linear_kernel<2, FMT, CB> : linear_kernel<4, FMT, CB>;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
   if (e != cudaSuccess) return e;
   return launch_pdl(kern, dim3(grid), dim3(kThreads), smem, s, a);
+}
+
+template <int CB>
+cudaError_t launch_stage(int fmt, const LinearArgs& a, int nt, int grid, size_t smem, cudaStream_t s) {
+  switch (fmt) {
+    case F_H32: return launch_fmt<F_H32, CB>(a, nt, grid, smem, s);
+    case F_H128: return launch_fmt<F_H128, CB>(a, nt, grid, smem, s);
+    case F_E32: return launch_fmt<F_E32, CB>(a, nt, grid, smem, s);
+    case F_H32_HALF: return launch_fmt<F_H32_HALF, CB>(a, nt, grid, smem, s);
+    default: return launch_fmt<F_H128_HALF, CB>(a, nt, grid, smem, s);
+  }
+}
+
+int groups_of_8(int tt) { return tt <= 8 ? 1 : tt <= 16 ? 2 : 4; }
+
+// The most tokens (up to 32) whose activations fit beside a ring.
+int most_tokens(int ring, int nb) {
+  int most = 0;
+  for (int tt = 1; tt <= 32; ++tt)
+    if (linear_smem(ring, nb, tt, groups_of_8(tt)) <= kMaxSmem) most = tt;
+  return most;
 }
 
 }  // namespace
@@ -416,33 +520,41 @@ cudaError_t launch_linear(const LinearCall& c, int num_sms, cudaStream_t s) {
   a.codes = c.codes; a.scales = c.scales; a.row_scales = c.row_scales; a.bias = c.bias; a.x = c.x; a.y = c.y;
   a.N = c.rows; a.K = c.cols; a.T = c.T;
   a.nb = c.cols / 32;
-  a.chunks = (c.cols + kChunk - 1) / kChunk;
+  a.spr = c.cols / c.block;
   a.x_type = c.x_type; a.y_type = c.y_type; a.gated = c.gated;
-  a.off = c.half_levels ? 7.5f : 8.f;
-  a.aligned = a.nb % 4 == 0;          // a stage's scales of a row start on a 4- or 8-byte boundary
-  // warps per row tile: as many as have columns to take, evenly
-  const int per = (a.chunks + kWarps - 1) / kWarps;
-  a.KG = (a.chunks + per - 1) / per;
-  a.groups = kWarps / a.KG;
-  // tokens of a slice: the most (up to 32) whose activations fit beside the ring
-  int most = 1;
-  for (int tt = 2; tt <= 32; ++tt) {
-    const int nt = tt <= 8 ? 1 : tt <= 16 ? 2 : 4;
-    if (linear_smem(a.nb, tt, nt) <= kMaxSmem) most = tt;
-  }
-  most = min(most, c.T);
+  const int fmt = c.scale_fmt == 1 ? F_E32
+                  : c.block == 128 ? (c.half_levels ? F_H128_HALF : F_H128)
+                                   : (c.half_levels ? F_H32_HALF : F_H32);
+  const int tiles = (a.N + 15) / 16;
+  // the wide stage unless it costs a token slice or there is too little work
+  // for every warp of the machine to fill one
+  const int most4 = min(c.T, most_tokens(Stage<4>::RING, a.nb)), most8 = min(c.T, most_tokens(Stage<8>::RING, a.nb));
+  const bool wide = most8 > 0 && (c.T + most8 - 1) / most8 == (c.T + most4 - 1) / most4 &&
+                    size_t(tiles) * ((a.nb + 7) / 8) >= size_t(num_sms) * kWarps;
+  const int CB = wide ? 8 : 4, most = wide ? most8 : most4;
+  a.chunks = (a.nb + CB - 1) / CB;
   a.ny = (c.T + most - 1) / most;
   a.tt = (c.T + a.ny - 1) / a.ny;
   a.ny = (c.T + a.tt - 1) / a.tt;
-  const int nt = a.tt <= 8 ? 1 : a.tt <= 16 ? 2 : 4;
-  const size_t smem = linear_smem(a.nb, a.tt, nt);
-  const int tiles = (a.N + 15) / 16;
-  const int want = (tiles + a.groups - 1) / a.groups;
-  const int gx = max(1, min(want, num_sms / a.ny));
-  const int grid = gx * a.ny;
-  if (c.scale_fmt == 1) return launch_fmt<F_E32>(a, nt, grid, smem, s);
-  if (c.block == 128) return launch_fmt<F_H128>(a, nt, grid, smem, s);
-  return launch_fmt<F_H32>(a, nt, grid, smem, s);
+  // Warps per row tile: the split whose busiest warp ends first.  A stage
+  // takes the time its bytes need at an even share of the memory rate; joining
+  // and storing a tile costs about half a narrow stage.
+  const int sms = max(1, num_sms / a.ny);
+  int best = 0;
+  for (int kg = 1; kg <= min(kWarps, a.chunks); ++kg) {
+    const int gr = min(kWarps / kg, (tiles + sms - 1) / sms);
+    const int rounds = (tiles + sms * gr - 1) / (sms * gr), stages = (a.chunks + kg - 1) / kg;
+    const int cost = rounds * (stages * 2 * (CB / 4) + 1);
+    if (best == 0 || cost < best) {
+      best = cost;
+      a.KG = kg;
+      a.groups = gr;
+    }
+  }
+  const int gx = min((tiles + a.groups - 1) / a.groups, sms);
+  const int nt = groups_of_8(a.tt);
+  const size_t smem = linear_smem(wide ? Stage<8>::RING : Stage<4>::RING, a.nb, a.tt, nt);
+  return wide ? launch_stage<8>(fmt, a, nt, gx * a.ny, smem, s) : launch_stage<4>(fmt, a, nt, gx * a.ny, smem, s);
 }
 
 }  // namespace moe
