@@ -89,10 +89,12 @@ __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commi
 template <int N>
 __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
-__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+// d = a b + c; c = 0 where the sum starts (zeros that stay in registers)
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, float c0,
+                                         float c1, float c2, float c3) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
 }
 
 // Eight codes as exact fp16 pairs (e_j, e_{j+4}), j = 0..3.  Integer levels:
@@ -151,10 +153,11 @@ __device__ __forceinline__ void stage_scales(const unsigned char* sc, int row, f
   }
 }
 
-// Shared memory: ring | x [nb][tt][4] 16-byte words | partial sums [groups
+// Shared memory: ring | x [tt][nb | 1][4] 16-byte words (an odd number of
+// blocks, so that two tokens' words fall into different banks) | partial sums [groups
 // KG][16][8 NT] floats | inv [8 NT] floats | row maxima [tt][16] u32.
 inline size_t linear_smem(int ring, int nb, int tt, int nt) {
-  return size_t(ring) + size_t(nb) * tt * 64 + size_t(kWarps) * 16 * 8 * nt * 4 + size_t(nt) * 32 + size_t(tt) * 64;
+  return size_t(ring) + size_t(nb | 1) * tt * 64 + size_t(kWarps) * 16 * 8 * nt * 4 + size_t(nt) * 32 + size_t(tt) * 64;
 }
 
 // Eight activations as fp16 pairs (j, j + 4), the order of `levels`.
@@ -183,21 +186,23 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const LinearArgs a)
   using F = Format<FMT>;
   using S = Stage<CB>;
   extern __shared__ __align__(128) unsigned char lsm[];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, int(threadIdx.x) >> 5, 0), lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
   const int nb = a.nb, tt = a.tt;
   constexpr int TP = 8 * NT;
   unsigned char* sx = lsm + S::RING;
-  float* spart = reinterpret_cast<float*>(sx + size_t(nb) * tt * 64);
+  float* spart = reinterpret_cast<float*>(sx + (nb | 1) * tt * 64);
   float* sinv = spart + kWarps * 16 * TP;
   uint32_t* smax = reinterpret_cast<uint32_t*>(sinv + TP);
 
+  const int xpitch = (nb | 1) * 64;
   const int slice = int(blockIdx.x % unsigned(a.ny)), cta = int(blockIdx.x / unsigned(a.ny));
   const int ctas = int(gridDim.x / unsigned(a.ny));
   const int t0 = slice * tt, nt = min(tt, a.T - t0);     // this CTA's tokens
   const int ntiles = (a.N + 15) >> 4;
   const int grp = warp / a.KG, kw = warp - grp * a.KG;
-  const int first = cta * a.groups + grp, step = ctas * a.groups;
+  // neighbouring tiles go to different CTAs, so that CTAs differ by one tile at most
+  const int first = grp * ctas + cta, step = ctas * a.groups;
   const int my_chunks = grp < a.groups ? (a.chunks - kw + a.KG - 1) / a.KG : 0;
   const int my_tiles = grp < a.groups && first < ntiles ? (ntiles - first + step - 1) / step : 0;
   const int total = my_tiles * my_chunks;
@@ -236,10 +241,20 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const LinearArgs a)
   const uint8_t* src = nullptr;      // this lane's piece of the next stage, row r0 of its tile
   const uint8_t* ssrc = nullptr;     // (direct) the scales of row `lane` of that tile
   int it_tile = first, it_chunk = 0, left = total, slot_i = 0;
-  bool ragged = false;               // the tile reaches past the last row
+  int row_off[CB / 2];               // from row r0 to this lane's other rows; rows past the end: the last one again
+  uint32_t dst_off[CB / 2];
+#pragma unroll
+  for (int i = 0; i < CB / 2; ++i) {
+    const int r = r0 + i * RS;
+    row_off[i] = i * RS * row_bytes;
+    dst_off[i] = r * S::ROW + ((ch ^ (CB == 8 ? r & 7 : (r >> 1) & 3)) << 4);
+  }
   auto enter_tile = [&]() {
     it_chunk = kw;
-    ragged = it_tile * 16 + 16 > a.N;
+    if (it_tile * 16 + 16 > a.N) {
+#pragma unroll
+      for (int i = 0; i < CB / 2; ++i) row_off[i] = min(i * RS, a.N - 1 - it_tile * 16 - r0) * row_bytes;
+    }
     src = a.codes + size_t(it_tile * 16 + r0) * row_bytes + size_t(kw) * S::ROW + ch * 16;
     ssrc = static_cast<const uint8_t*>(a.scales) +
            (size_t(min(it_tile * 16 + (lane & 15), a.N - 1)) * a.spr + size_t(kw) * SPC) * F::SB;
@@ -249,14 +264,9 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const LinearArgs a)
     if (!direct) flush_pending();
     if (left > 0) {
       const uint32_t dst = ring_s + slot_i * S::BYTES;
-      const bool in = it_chunk * CB + ch < nb;            // the last stage of a row may be short
+      if (it_chunk * CB + ch < nb) {                      // the last stage of a row may be short
 #pragma unroll
-      for (int i = 0; i < CB / 2; ++i) {
-        const int r = r0 + i * RS;
-        int sr = i * RS;
-        if (ragged) sr = min(sr, a.N - 1 - it_tile * 16 - r0);       // rows past the end: the last one again
-        if (in)
-          cp_async16(dst + r * S::ROW + ((ch ^ (CB == 8 ? r & 7 : (r >> 1) & 3)) << 4), src + ptrdiff_t(sr) * row_bytes);
+        for (int i = 0; i < CB / 2; ++i) cp_async16(dst + dst_off[i], src + row_off[i]);
       }
       if (direct) {
         if (lane < 16) {
@@ -359,8 +369,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const LinearArgs a)
         for (int i = 0; i < HOLD; ++i) {
           const int w = w0 + i * 32 + lane;
           if (w < end)
-            *reinterpret_cast<uint4*>(sx + (size_t(w >> 2) * tt + n) * 64 + (w & 3) * 16) =
-                pack_activations(hold[i], bf, mul);
+            *reinterpret_cast<uint4*>(sx + n * xpitch + w * 16) = pack_activations(hold[i], bf, mul);
         }
       }
     }
@@ -373,8 +382,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const LinearArgs a)
   // none: those columns are never stored)
   const unsigned char* xrow[NT];
 #pragma unroll
-  for (int j = 0; j < NT; ++j) xrow[j] = sx + min(8 * j + g, nt - 1) * 64 + t * 16;
-  const int xstep = tt * 64;
+  for (int j = 0; j < NT; ++j) xrow[j] = sx + min(8 * j + g, nt - 1) * xpitch + t * 16;
+  const uint32_t lane_code = uint32_t(g * S::ROW + ((CB == 8 ? g : (g >> 1) & 3) << 4) + t * 4);
   float acc[NT][4];
 #pragma unroll
   for (int j = 0; j < NT; ++j)
@@ -394,27 +403,24 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const LinearArgs a)
     stage_scales<FMT, CB>(st + S::CODES, g, s0);
     stage_scales<FMT, CB>(st + S::CODES, g + 8, s1);
     const int nblk = min(CB, nb - chunk * CB);
-    const unsigned char* code0 = st + g * S::ROW + t * 4;
-    const int sw = CB == 8 ? g : (g >> 1) & 3;            // rows g and g + 8 share the swizzle
+    // rows g and g + 8 share the swizzle; a stage's offset is a multiple of 128
+    const uint32_t code0 = uint32_t(st - lsm) + lane_code;
     const unsigned char* xc[NT];
 #pragma unroll
-    for (int j = 0; j < NT; ++j) xc[j] = xrow[j] + chunk * CB * xstep;
+    for (int j = 0; j < NT; ++j) xc[j] = xrow[j] + chunk * (CB * 64);
     float d[NT][4];
     // fold: the sums so far take the scale of block b
     auto block = [&](int b, bool start, bool fold) {
       uint32_t q0[4], q1[4];
-      levels<F::HALF>(*reinterpret_cast<const uint32_t*>(code0 + ((b ^ sw) << 4)), q0);
-      levels<F::HALF>(*reinterpret_cast<const uint32_t*>(code0 + 8 * S::ROW + ((b ^ sw) << 4)), q1);
+      levels<F::HALF>(*reinterpret_cast<const uint32_t*>(lsm + (code0 ^ (b << 4))), q0);
+      levels<F::HALF>(*reinterpret_cast<const uint32_t*>(lsm + (code0 ^ (b << 4)) + 8 * S::ROW), q1);
       const uint32_t lo[4] = {q0[0], q1[0], q0[1], q1[1]}, hi[4] = {q0[2], q1[2], q0[3], q1[3]};
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
-        const uint4 xv = *reinterpret_cast<const uint4*>(xc[j] + b * xstep);
-        if (start) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) d[j][i] = 0.f;
-        }
-        mma16816(d[j], lo, xv.x, xv.y);
-        mma16816(d[j], hi, xv.z, xv.w);
+        const uint4 xv = *reinterpret_cast<const uint4*>(xc[j] + b * 64);
+        if (start) mma16816(d[j], lo, xv.x, xv.y, 0.f, 0.f, 0.f, 0.f);
+        else mma16816(d[j], lo, xv.x, xv.y, d[j][0], d[j][1], d[j][2], d[j][3]);
+        mma16816(d[j], hi, xv.z, xv.w, d[j][0], d[j][1], d[j][2], d[j][3]);
         if (fold) {
           acc[j][0] = fmaf(s0[b], d[j][0], acc[j][0]);
           acc[j][1] = fmaf(s0[b], d[j][1], acc[j][1]);
@@ -536,15 +542,16 @@ cudaError_t launch_linear(const LinearCall& c, int num_sms, cudaStream_t s) {
   a.ny = (c.T + most - 1) / most;
   a.tt = (c.T + a.ny - 1) / a.ny;
   a.ny = (c.T + a.tt - 1) / a.tt;
-  // Warps per row tile: the split whose busiest warp ends first.  A stage
-  // takes the time its bytes need at an even share of the memory rate; joining
-  // and storing a tile costs about half a narrow stage.
-  const int sms = max(1, num_sms / a.ny);
+  // Warps per row tile: the split that ends first.  In cycles, roughly, and
+  // per narrow stage: an SM that is full delivers one every 60; a warp alone
+  // takes 250; joining and storing a tile takes a warp 200, and the SM 20 for
+  // each warp that joins.
+  const int sms = max(1, num_sms / a.ny), per_sm = (tiles + sms - 1) / sms;
   int best = 0;
   for (int kg = 1; kg <= min(kWarps, a.chunks); ++kg) {
-    const int gr = min(kWarps / kg, (tiles + sms - 1) / sms);
-    const int rounds = (tiles + sms * gr - 1) / (sms * gr), stages = (a.chunks + kg - 1) / kg;
-    const int cost = rounds * (stages * 2 * (CB / 4) + 1);
+    const int gr = min(kWarps / kg, per_sm), w = CB / 4;
+    const int rounds = (per_sm + gr - 1) / gr, stages = (a.chunks + kg - 1) / kg;
+    const int cost = max(per_sm * (a.chunks * w * 60 + kg * 20), rounds * (stages * w * 250 + 200));
     if (best == 0 || cost < best) {
       best = cost;
       a.KG = kg;
