@@ -303,35 +303,54 @@ def linear_config_of(bits=4, block=32, half_levels=False, fp8_scales=False) -> M
     return MoeConfig(bits=bits, block=block, half_levels=1 if half_levels else 0, scale_fmt=1 if fp8_scales else 0)
 
 
-def _dense(what: str, device, **tensors):
-    """Every given tensor dense and on `device`; the C entry sees only pointers."""
-    for name, t in tensors.items():
+_types = None        # torch dtype -> moe_type, filled by the first call (torch is imported then)
+_raw_stream = None   # device index -> handle of its current stream
+
+
+def _torch_types():
+    global _types, _raw_stream
+    if _types is None:
+        import torch
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda i: torch.cuda.current_stream(i).cuda_stream)
+        _types = {torch.bfloat16: MOE_BF16, torch.float16: MOE_FP16, torch.float32: MOE_FP32}
+    return _types
+
+
+def _dense(what: str, names: str, tensors) -> int:
+    """Every given tensor dense and on one CUDA device, whose index is
+    returned; the C entry sees only pointers."""
+    dev = None
+    for i, t in enumerate(tensors):
         if t is None:
             continue
-        if t.device != device:
-            raise ValueError(f"{what}: {name} is on {t.device}, x on {device}")
-        if not t.is_contiguous():
-            raise ValueError(f"{what}: {name} is not contiguous")
+        d = t.get_device()
+        if dev is None:
+            dev = d
+        if d != dev or d < 0 or not t.is_contiguous():
+            name = names.split()[i]
+            if not t.is_contiguous():
+                raise ValueError(f"{what}: {name} is not contiguous")
+            raise ValueError(f"{what}: {name} is on {t.device}: all tensors have to be on one CUDA device")
+    return dev
 
 
 def _type_of(what: str, name: str, t, fp32: bool = False) -> int:
-    import torch
-    code = {torch.bfloat16: MOE_BF16, torch.float16: MOE_FP16, torch.float32: MOE_FP32 if fp32 else None}.get(t.dtype)
-    if code is None:
+    code = _torch_types().get(t.dtype)
+    if code is None or (code == MOE_FP32 and not fp32):
         raise ValueError(f"{what}: {name} has type {t.dtype}")
     return code
 
 
-def _on_device(device, stream, call):
-    """call(stream handle) with `device` current; without a stream, on that
-    device's current stream."""
+def _on_device(dev: int, stream, entry, *args) -> int:
+    """entry(*args, stream handle) with device `dev` current; without a stream,
+    on that device's current stream."""
     import torch
-    if device.type != "cuda":
-        raise ValueError(f"x is on {device}: a CUDA tensor is needed")
-    if device.index == torch.cuda.current_device():
-        return call(_stream(stream))
-    with torch.cuda.device(device):
-        return call(_stream(stream))
+    _torch_types()
+    if torch.cuda.current_device() != dev:
+        with torch.cuda.device(dev):
+            return entry(*args, _raw_stream(dev) if stream is None else _stream(stream))
+    return entry(*args, _raw_stream(dev) if stream is None else _stream(stream))
 
 
 def _packed(what: str, cfg: MoeConfig, codes, scales, row_scales, rows: int, cols: int):
@@ -345,42 +364,39 @@ def _packed(what: str, cfg: MoeConfig, codes, scales, row_scales, rows: int, col
         raise ValueError(f"{what}: row_scales are not {rows} fp32 values")
 
 
+def _linear(what: str, entry, cfg: MoeConfig, codes, scales, row_scales, bias, x, y, per_out: int, stream, check) -> int:
+    """Both packed products: per_out rows of the matrix for each output column."""
+    if x.dim() != 2 or y.dim() != 2 or x.shape[0] != y.shape[0]:
+        raise ValueError(f"{what}: x is {tuple(x.shape)}, the output {tuple(y.shape)}")
+    (T, cols), out = x.shape, y.shape[1]
+    _packed(what, cfg, codes, scales, row_scales, per_out * out, cols)
+    xt, yt = _type_of(what, "x", x), _type_of(what, "the output", y, fp32=True)
+    head = (ctypes.byref(cfg), codes.data_ptr(), scales.data_ptr(), _ptr(row_scales), out, cols)
+    tail = (x.data_ptr(), xt, T, y.data_ptr(), yt)
+    if per_out == 1:
+        if bias is not None and (bias.numel() != out or bias.element_size() != 4):
+            raise ValueError(f"{what}: bias is not {out} fp32 values")
+        head += (_ptr(bias),)
+    dev = _dense(what, "x output codes scales row_scales bias", (x, y, codes, scales, row_scales, bias))
+    st = _on_device(dev, stream, entry, *head, *tail)
+    if check and st != MOE_OK:
+        _check(st, what)
+    return st
+
+
 def moe_linear_forward(cfg: MoeConfig, codes, scales, x, y, *, row_scales=None, bias=None, stream=None,
                        check=True) -> int:
     """y [T][rows] = x [T][cols] times the packed matrix's transpose (+ bias
     [rows] fp32).  x bf16 or fp16; y bf16, fp16 or fp32."""
-    what = "moe_linear_forward"
-    _dense(what, x.device, codes=codes, scales=scales, x=x, y=y, row_scales=row_scales, bias=bias)
-    (T, cols), rows = x.shape, y.shape[-1]
-    if y.shape != (T, rows):
-        raise ValueError(f"{what}: y is {tuple(y.shape)} for {T} rows of x")
-    _packed(what, cfg, codes, scales, row_scales, rows, cols)
-    if bias is not None and (bias.numel() != rows or bias.element_size() != 4):
-        raise ValueError(f"{what}: bias is not {rows} fp32 values")
-    xt, yt = _type_of(what, "x", x), _type_of(what, "y", y, fp32=True)
-    st = _on_device(x.device, stream, lambda s: load_library().moe_linear_forward(
-        ctypes.byref(cfg), _ptr(codes), _ptr(scales), _ptr(row_scales), rows, cols, _ptr(bias), _ptr(x), xt, T,
-        _ptr(y), yt, s))
-    if check:
-        _check(st, what)
-    return st
+    return _linear("moe_linear_forward", load_library().moe_linear_forward, cfg, codes, scales, row_scales, bias, x, y, 1,
+                   stream, check)
 
 
 def moe_linear_gated_forward(cfg: MoeConfig, codes, scales, x, h, *, row_scales=None, stream=None, check=True) -> int:
     """h [T][I] = silu(x W_gate^T) * (x W_up^T) for a packed matrix of 2I rows,
     row 2i = gate row i, row 2i + 1 = up row i."""
-    what = "moe_linear_gated_forward"
-    _dense(what, x.device, codes=codes, scales=scales, x=x, h=h, row_scales=row_scales)
-    (T, cols), inter = x.shape, h.shape[-1]
-    if h.shape != (T, inter):
-        raise ValueError(f"{what}: h is {tuple(h.shape)} for {T} rows of x")
-    _packed(what, cfg, codes, scales, row_scales, 2 * inter, cols)
-    xt, ht = _type_of(what, "x", x), _type_of(what, "h", h, fp32=True)
-    st = _on_device(x.device, stream, lambda s: load_library().moe_linear_gated_forward(
-        ctypes.byref(cfg), _ptr(codes), _ptr(scales), _ptr(row_scales), inter, cols, _ptr(x), xt, T, _ptr(h), ht, s))
-    if check:
-        _check(st, what)
-    return st
+    return _linear("moe_linear_gated_forward", load_library().moe_linear_gated_forward, cfg, codes, scales, row_scales,
+                   None, x, h, 2, stream, check)
 
 
 def moe_ffn_workspace_bytes(hidden: int, inter: int, max_tokens: int, backward: bool = False) -> int:
@@ -389,16 +405,19 @@ def moe_ffn_workspace_bytes(hidden: int, inter: int, max_tokens: int, backward: 
 
 def _ffn_sizes(what: str, w_gate_up, w_down, x, **others):
     """(hidden, inter, T, type) of a block, every array checked against them."""
+    if x.dim() != 2 or w_down.dim() != 2:
+        raise ValueError(f"{what}: x is {tuple(x.shape)}, w_down {tuple(w_down.shape)}")
     hidden, inter = w_down.shape
-    T = x.shape[0]
-    want = {"w_gate_up": (2 * inter, hidden), "x": (T, hidden), "y": (T, hidden), "dy": (T, hidden),
-            "dx": (T, hidden), "dw_gate_up": (2 * inter, hidden), "dw_down": (hidden, inter)}
-    arrays = {"w_gate_up": w_gate_up, "x": x, **others}
-    for name, t in arrays.items():
-        if t is not None and (tuple(t.shape) != want[name] or t.dtype != x.dtype):
-            raise ValueError(f"{what}: {name} is {tuple(t.shape)} of {t.dtype}, not {want[name]} of {x.dtype}")
-    if w_down.dtype != x.dtype:
-        raise ValueError(f"{what}: w_down has type {w_down.dtype}, x {x.dtype}")
+    T, dtype = x.shape[0], x.dtype
+    if w_down.dtype != dtype:
+        raise ValueError(f"{what}: w_down has type {w_down.dtype}, x {dtype}")
+    for name, t in (("w_gate_up", w_gate_up), ("x", x), *others.items()):
+        if t is None:
+            continue
+        want = ((2 * inter, hidden) if name.endswith("w_gate_up") else
+                (hidden, inter) if name == "dw_down" else (T, hidden))
+        if t.shape != want or t.dtype != dtype:
+            raise ValueError(f"{what}: {name} is {tuple(t.shape)} of {t.dtype}, not {want} of {dtype}")
     return hidden, inter, T, _type_of(what, "x", x)
 
 
@@ -406,10 +425,10 @@ def moe_ffn_forward(w_gate_up, w_down, x, y, workspace, *, stream=None, check=Tr
     """y [T][H] = (silu(x Wg^T) * (x Wu^T)) Wd^T on 16-bit weights: w_gate_up
     [2I][H] with gate and up rows interleaved, w_down [H][I]."""
     what = "moe_ffn_forward"
-    _dense(what, x.device, w_gate_up=w_gate_up, w_down=w_down, x=x, y=y, workspace=workspace)
+    dev = _dense(what, "w_gate_up w_down x y workspace", (w_gate_up, w_down, x, y, workspace))
     hidden, inter, T, ty = _ffn_sizes(what, w_gate_up, w_down, x, y=y)
-    st = _on_device(x.device, stream, lambda s: load_library().moe_ffn_forward(
-        hidden, inter, ty, _ptr(w_gate_up), _ptr(w_down), _ptr(x), T, _ptr(y), _ptr(workspace), _nbytes(workspace), s))
+    st = _on_device(dev, stream, load_library().moe_ffn_forward, hidden, inter, ty, w_gate_up.data_ptr(),
+                    w_down.data_ptr(), x.data_ptr(), T, y.data_ptr(), workspace.data_ptr(), _nbytes(workspace))
     if check:
         _check(st, what)
     return st
@@ -420,12 +439,12 @@ def moe_ffn_backward(w_gate_up, w_down, x, dy, workspace, *, dx=None, dw_gate_up
     """Gradients of moe_ffn_forward for dy [T][H]; the ones given as tensors are
     overwritten, the others are not computed."""
     what = "moe_ffn_backward"
-    _dense(what, x.device, w_gate_up=w_gate_up, w_down=w_down, x=x, dy=dy, workspace=workspace, dx=dx,
-           dw_gate_up=dw_gate_up, dw_down=dw_down)
+    dev = _dense(what, "w_gate_up w_down x dy workspace dx dw_gate_up dw_down",
+                 (w_gate_up, w_down, x, dy, workspace, dx, dw_gate_up, dw_down))
     hidden, inter, T, ty = _ffn_sizes(what, w_gate_up, w_down, x, dy=dy, dx=dx, dw_gate_up=dw_gate_up, dw_down=dw_down)
-    st = _on_device(x.device, stream, lambda s: load_library().moe_ffn_backward(
-        hidden, inter, ty, _ptr(w_gate_up), _ptr(w_down), _ptr(x), _ptr(dy), T, _ptr(dx), _ptr(dw_gate_up),
-        _ptr(dw_down), _ptr(workspace), _nbytes(workspace), s))
+    st = _on_device(dev, stream, load_library().moe_ffn_backward, hidden, inter, ty, w_gate_up.data_ptr(),
+                    w_down.data_ptr(), x.data_ptr(), dy.data_ptr(), T, _ptr(dx), _ptr(dw_gate_up), _ptr(dw_down),
+                    workspace.data_ptr(), _nbytes(workspace))
     if check:
         _check(st, what)
     return st
