@@ -93,17 +93,17 @@ __device__ __forceinline__ void arrive_leader(uint64_t* bar) {
 // Tensor copy into this SM's shared memory, completing on `bar` (this SM's
 // barrier, or with a pair the first SM's).
 template <int CG>
-__device__ __forceinline__ void load_box(void* dst, const CUtensorMap* map, int c0, int c1, uint32_t bar) {
+__device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap* map, int c0, int c1, uint32_t bar) {
   if (CG == 1)
     asm volatile(
         "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
-        ::"r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar)
+        ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar)
         : "memory");
   else
     asm volatile(
         "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
         " [%0], [%1, {%2, %3}], [%4];"
-        ::"r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar)
+        ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar)
         : "memory");
 }
 template <int CG>
@@ -163,7 +163,7 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t v[16]) {
 // 1024 bytes apart, 16 deep = 32 bytes on).  Contiguous along the rows: boxes
 // of 64 rows (128 bytes) x 64 deep, 8 KB apart; 8-deep atoms 1024 bytes apart,
 // 16 deep = 2048 bytes on.
-__device__ __forceinline__ uint64_t operand_desc(uint32_t saddr, int mn) {
+__device__ __forceinline__ uint64_t operand_desc(uint32_t saddr, bool mn) {
   const uint64_t d = sw128_desc(saddr);
   return mn ? (d & ~(uint64_t(0x3FFF) << 16)) | (uint64_t(8192 >> 4) << 16) : d;
 }
@@ -172,24 +172,76 @@ __device__ __forceinline__ uint32_t instr_desc(int bf16, int a_mn, int b_mn, int
   return (1u << 4) | (uint32_t(bf16) << 7) | (uint32_t(bf16) << 10) | (uint32_t(a_mn) << 15) | (uint32_t(b_mn) << 16) |
          (uint32_t(n >> 3) << 17) | (uint32_t(m >> 4) << 24);
 }
-// The 64-deep step of one stage: four instructions.
-template <int CG>
-__device__ __forceinline__ void mma_stage(uint32_t d, uint32_t sa, uint32_t sb, int a_mn, int b_mn, uint32_t idesc,
-                                          bool first) {
-  const uint64_t ad = operand_desc(sa, a_mn), bd = operand_desc(sb, b_mn);
-  const uint32_t as = a_mn ? 2048 >> 4 : 32 >> 4, bs = b_mn ? 2048 >> 4 : 32 >> 4;
-#pragma unroll
-  for (int k = 0; k < BK / 16; ++k) mma<CG>(d, ad + k * as, bd + k * bs, idesc, (first && k == 0) ? 0u : 1u);
-}
-// One operand of a stage: `rows` rows from row0, 64 deep from k0.
-template <int CG>
-__device__ __forceinline__ void load_operand(unsigned char* dst, const CUtensorMap* map, int mn, int row0, int rows,
-                                             int k0, uint32_t bar) {
-  if (!mn) {
+// A ring position: slot and the parity its full barrier turns to.
+template <int N>
+struct Cursor {
+  int s = 0;
+  uint32_t parity = 0;
+  __device__ __forceinline__ void next() {
+    if (++s == N) { s = 0; parity ^= 1u; }
+  }
+};
+
+// One operand of a stage, ROWS rows from row0 and 64 deep from k0: one box, or
+// boxes of 64 rows when it is contiguous along them.
+template <int CG, bool MN, int ROWS>
+__device__ __forceinline__ void load_operand(uint32_t dst, const CUtensorMap* map, int row0, int k0, uint32_t bar) {
+  if (!MN) {
     load_box<CG>(dst, map, k0, row0, bar);
   } else {
-    for (int r = 0; r < rows; r += 64) load_box<CG>(dst + r * 128, map, row0 + r, k0, bar);
+#pragma unroll
+    for (int r = 0; r < ROWS; r += 64) load_box<CG>(dst + r * 128, map, row0 + r, k0, bar);
   }
+}
+// The copies of `steps` stages of one tile by one thread.  The loop has to be
+// short: it runs at one thread's latency, and every cycle above the products'
+// own time is lost (divisions and run-time operand orders in it made a step
+// take 800 cycles instead of 512).  False when a slot never became free.
+template <int CG, bool AMN, bool BMN, int BROWS, int STAGE, int STAGES>
+__device__ __forceinline__ bool load_steps(uint32_t ring, uint64_t* full, uint64_t* empty, uint32_t full_leader, int rank,
+                                           Cursor<STAGES>& c, const CUtensorMap* ma, const CUtensorMap* mb, int row_a,
+                                           int row_b, int steps, const volatile int* abort_flag) {
+  for (int kb = 0; kb < steps; ++kb) {
+    if (!mbar_wait(&empty[c.s], c.parity ^ 1u, abort_flag)) return false;
+    if (rank == 0) mbar_arrive_expect_tx(&full[c.s], CG * (kAStage + BROWS * 128));
+    const uint32_t st = ring + uint32_t(c.s) * STAGE, bar = full_leader + uint32_t(c.s) * 8;
+    load_operand<CG, AMN, 128>(st, ma, row_a, kb * BK, bar);
+    load_operand<CG, BMN, BROWS>(st + kAStage, mb, row_b, kb * BK, bar);
+    c.next();
+  }
+  return true;
+}
+// The products of `steps` stages into the accumulator at d, by one warp: one
+// lane issues.  A stage is four instructions of 16 deep.
+template <int CG, bool AMN, bool BMN, int STAGE, int STAGES>
+__device__ __forceinline__ bool mma_steps(uint32_t ring, uint64_t* full, uint64_t* empty, Cursor<STAGES>& c, uint32_t d,
+                                          uint32_t idesc, int steps, uint64_t* done, const volatile int* abort_flag) {
+  const uint64_t ad0 = operand_desc(ring, AMN), bd0 = operand_desc(ring + kAStage, BMN);
+  constexpr int as = (AMN ? 2048 : 32) >> 4, bs = (BMN ? 2048 : 32) >> 4;
+  for (int kb = 0; kb < steps; ++kb) {
+    if (!__all_sync(0xffffffffu, mbar_wait(&full[c.s], c.parity, abort_flag))) return false;
+    tc_fence_after();
+    const uint64_t at = uint64_t(uint32_t(c.s) * (STAGE >> 4));
+    if (elect_one()) {
+#pragma unroll
+      for (int k = 0; k < BK / 16; ++k) mma<CG>(d, ad0 + at + k * as, bd0 + at + k * bs, idesc, (kb | k) ? 1u : 0u);
+      commit<CG>(&empty[c.s]);
+      if (kb == steps - 1) commit<CG>(done);
+    }
+    __syncwarp();
+    c.next();
+  }
+  return true;
+}
+// Waits for the last phase that each slot's barrier was used for.  Before an
+// SM leaves: on the empty barriers, so that neither a copy nor a release of a
+// stage is under way (with a pair, the first SM's copies of both have landed
+// before that); after a wait gave up, on the full ones.
+template <int STAGES>
+__device__ __forceinline__ bool settled(uint64_t* bars, Cursor<STAGES> c) {
+  bool ok = true;
+  for (int i = 0; i < STAGES; ++i, c.next()) ok = mbar_wait(&bars[c.s], c.parity ^ 1u, nullptr) && ok;
+  return ok;
 }
 
 __device__ __forceinline__ uint32_t pack2(float a, float b, int bf16) {
@@ -222,6 +274,8 @@ __device__ __forceinline__ void tile_of(const Problem& p, int l, int* m, int* n)
 }
 
 enum { EPI_STORE = 0, EPI_GATED = 1 };
+struct Yes { static constexpr bool value = true; };
+struct No { static constexpr bool value = false; };
 constexpr int kEpiWarps = 8;
 constexpr int kGemmThreads = (kEpiWarps + 2) * 32;
 
@@ -271,64 +325,43 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ffn_gemm_kernel(const __grid_
 
   if (warp == kEpiWarps && lane == 0) {
     // ------------------------------------------------------- producer
-    int kc = 0;
-    for (int t = unit; t < a.ntiles && !*abort_flag; t += units) {
+    Cursor<T::STAGES> c;
+    const uint32_t ring = smem_u32(base), leader = CG == 1 ? smem_u32(full) : in_leader(full);
+    bool ok = true;
+    for (int t = unit; t < a.ntiles && ok; t += units) {
       int m, n;
       const int i = find(t, &m, &n);
       const Problem& p = a.p[i];
-      for (int kb = 0; kb < p.kblocks; ++kb, ++kc) {
-        const int s = kc % T::STAGES;
-        if (kc >= T::STAGES && !mbar_wait(&empty[s], ((kc / T::STAGES) - 1) & 1, abort_flag)) {
-          *abort_flag = 1; report_error(a.status, MOE_ERR_TIMEOUT, 50); break;
-        }
-        unsigned char* st = base + size_t(s) * T::STAGE;
-        if (rank == 0) mbar_arrive_expect_tx(&full[s], CG * T::STAGE);
-        const uint32_t bar = CG == 1 ? smem_u32(&full[s]) : in_leader(&full[s]);
-        load_operand<CG>(st, &maps.a[i], p.a_mn, m * T::BM + rank * 128, 128, kb * BK, bar);
-        load_operand<CG>(st + kAStage, &maps.b[i], p.b_mn, n * BN + rank * T::BROWS, T::BROWS, kb * BK, bar);
-      }
+      const int row_a = m * T::BM + rank * 128, row_b = n * BN + rank * T::BROWS;
+      auto run = [&](auto amn, auto bmn) {
+        return load_steps<CG, amn.value, bmn.value, T::BROWS, T::STAGE, T::STAGES>(
+            ring, full, empty, leader, rank, c, &maps.a[i], &maps.b[i], row_a, row_b, p.kblocks, abort_flag);
+      };
+      ok = p.a_mn ? run(Yes(), Yes()) : p.b_mn ? run(No(), Yes()) : run(No(), No());
     }
-    // no copy and no release of a stage is under way when this SM leaves
-    for (int i = max(0, kc - T::STAGES); i < kc; ++i) {
-      const int s = i % T::STAGES;
-      bool ok = rank != 0 || mbar_wait(&full[s], (i / T::STAGES) & 1, nullptr);
-      ok = ok && (*abort_flag || mbar_wait(&empty[s], (i / T::STAGES) & 1, abort_flag));
-      if (!ok) report_error(a.status, MOE_ERR_TIMEOUT, 51);
-    }
+    if (!ok) { *abort_flag = 1; report_error(a.status, MOE_ERR_TIMEOUT, 50); }
+    if (ok ? !settled(empty, c) : rank == 0 && !settled(full, c)) report_error(a.status, MOE_ERR_TIMEOUT, 51);
   } else if (warp == kEpiWarps + 1 && rank == 0) {
     // --------------------------------------------------------- issuer
-    int kc = 0, tc = 0;
+    Cursor<T::STAGES> c;
+    const uint32_t ring = smem_u32(base);
+    int tc = 0;
     bool ok = true;
     for (int t = unit; t < a.ntiles && ok; t += units, ++tc) {
-      if (__any_sync(0xffffffffu, *abort_flag != 0)) break;
       int m, n;
-      const int i = find(t, &m, &n);
-      const Problem& p = a.p[i];
+      const Problem& p = a.p[find(t, &m, &n)];
       const int buf = tc & 1;
-      if (tc >= 2) ok = __all_sync(0xffffffffu, mbar_wait(&acc_empty[buf], ((tc >> 1) - 1) & 1, abort_flag));
-      if (!ok) {
-        if (lane == 0) { *abort_flag = 1; report_error(a.status, MOE_ERR_TIMEOUT, 52); }
-        break;
-      }
+      ok = __all_sync(0xffffffffu, mbar_wait(&acc_empty[buf], ((tc >> 1) & 1) ^ 1, abort_flag));
+      if (!ok) break;
       tc_fence_after();
       const uint32_t idesc = instr_desc(a.bf16, p.a_mn, p.b_mn, T::BM, BN);
-      for (int kb = 0; kb < p.kblocks; ++kb, ++kc) {
-        const int s = kc % T::STAGES;
-        ok = __all_sync(0xffffffffu, mbar_wait(&full[s], (kc / T::STAGES) & 1, abort_flag));
-        if (!ok) {
-          if (lane == 0) { *abort_flag = 1; report_error(a.status, MOE_ERR_TIMEOUT, 53); }
-          break;
-        }
-        tc_fence_after();
-        const uint32_t sa = smem_u32(base + size_t(s) * T::STAGE);
-        if (elect_one()) {
-          mma_stage<CG>(tmem + uint32_t(buf * BN), sa, sa + kAStage, p.a_mn, p.b_mn, idesc, kb == 0);
-          commit<CG>(&empty[s]);
-          if (kb == p.kblocks - 1) commit<CG>(&acc_full[buf]);
-        }
-        __syncwarp();
-      }
+      auto run = [&](auto amn, auto bmn) {
+        return mma_steps<CG, amn.value, bmn.value, T::STAGE, T::STAGES>(ring, full, empty, c, tmem + uint32_t(buf * BN),
+                                                                       idesc, p.kblocks, &acc_full[buf], abort_flag);
+      };
+      ok = p.a_mn ? run(Yes(), Yes()) : p.b_mn ? run(No(), Yes()) : run(No(), No());
     }
+    if (!ok && lane == 0) { *abort_flag = 1; report_error(a.status, MOE_ERR_TIMEOUT, 52); }
   } else if (warp < kEpiWarps) {
     // ------------------------------------------------------- epilogue
     const int q = warp & 3, half = warp >> 2;
@@ -411,7 +444,6 @@ __global__ void __launch_bounds__(kGradThreads, 1) ffn_grad_kernel(const __grid_
                                                                    const __grid_constant__ CUtensorMap tm_wd) {
   using T = Tile<CG, 2 * NI>;
   constexpr int DROWS = NI / CG;                  // Wd columns that one SM brings
-  constexpr int D_STAGE = kAStage + DROWS * 128;
   static_assert(DROWS % 64 == 0, "Wd comes in boxes of 64 columns");
   extern __shared__ __align__(1024) unsigned char fsm[];
   unsigned char* base = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(fsm) + 1023) & ~uintptr_t(1023));
@@ -454,72 +486,41 @@ __global__ void __launch_bounds__(kGradThreads, 1) ffn_grad_kernel(const __grid_
   shape.tiles_n = a.tiles_n;
 
   if (warp == kGradEpi && lane == 0) {
-    int kc = 0;
-    for (int t = unit; t < ntiles && !*abort_flag; t += units) {
+    Cursor<T::STAGES> c;
+    const uint32_t ring = smem_u32(base), leader = CG == 1 ? smem_u32(full) : in_leader(full);
+    bool ok = true;
+    for (int t = unit; t < ntiles && ok; t += units) {
       int m, n;
       tile_of(shape, t, &m, &n);
-      for (int kb = 0; kb < 2 * a.kblocks; ++kb, ++kc) {
-        const int s = kc % T::STAGES;
-        if (kc >= T::STAGES && !mbar_wait(&empty[s], ((kc / T::STAGES) - 1) & 1, abort_flag)) {
-          *abort_flag = 1; report_error(a.status, MOE_ERR_TIMEOUT, 60); break;
-        }
-        unsigned char* st = base + size_t(s) * T::STAGE;
-        const bool second = kb >= a.kblocks;
-        const int k0 = (second ? kb - a.kblocks : kb) * BK, row0 = m * T::BM + rank * 128;
-        if (rank == 0) mbar_arrive_expect_tx(&full[s], CG * (second ? D_STAGE : T::STAGE));
-        const uint32_t bar = CG == 1 ? smem_u32(&full[s]) : in_leader(&full[s]);
-        if (!second) {
-          load_operand<CG>(st, &tm_x, 0, row0, 128, k0, bar);
-          load_operand<CG>(st + kAStage, &tm_wgu, 0, n * 2 * NI + rank * T::BROWS, T::BROWS, k0, bar);
-        } else {
-          load_operand<CG>(st, &tm_dy, 0, row0, 128, k0, bar);
-          load_operand<CG>(st + kAStage, &tm_wd, 1, n * NI + rank * DROWS, DROWS, k0, bar);
-        }
-      }
+      const int row_a = m * T::BM + rank * 128;
+      ok = load_steps<CG, false, false, T::BROWS, T::STAGE, T::STAGES>(ring, full, empty, leader, rank, c, &tm_x, &tm_wgu,
+                                                                      row_a, n * 2 * NI + rank * T::BROWS, a.kblocks,
+                                                                      abort_flag) &&
+           load_steps<CG, false, true, DROWS, T::STAGE, T::STAGES>(ring, full, empty, leader, rank, c, &tm_dy, &tm_wd,
+                                                                  row_a, n * NI + rank * DROWS, a.kblocks, abort_flag);
     }
-    // no copy and no release of a stage is under way when this SM leaves
-    for (int i = max(0, kc - T::STAGES); i < kc; ++i) {
-      const int s = i % T::STAGES;
-      bool ok = rank != 0 || mbar_wait(&full[s], (i / T::STAGES) & 1, nullptr);
-      ok = ok && (*abort_flag || mbar_wait(&empty[s], (i / T::STAGES) & 1, abort_flag));
-      if (!ok) report_error(a.status, MOE_ERR_TIMEOUT, 61);
-    }
+    if (!ok) { *abort_flag = 1; report_error(a.status, MOE_ERR_TIMEOUT, 60); }
+    if (ok ? !settled(empty, c) : rank == 0 && !settled(full, c)) report_error(a.status, MOE_ERR_TIMEOUT, 61);
   } else if (warp == kGradEpi + 1 && rank == 0) {
-    int kc = 0, tc = 0;
+    Cursor<T::STAGES> c;
+    const uint32_t ring = smem_u32(base);
+    const uint32_t id_gu = instr_desc(a.bf16, 0, 0, T::BM, 2 * NI), id_dh = instr_desc(a.bf16, 0, 1, T::BM, NI);
+    int tc = 0;
     bool ok = true;
     for (int t = unit; t < ntiles && ok; t += units, ++tc) {
-      if (__any_sync(0xffffffffu, *abort_flag != 0)) break;
       const int buf = tc & 1;
-      for (int ph = 0; ph < 2 && ok; ++ph) {
-        if (ph == 0 && tc >= 1)
-          ok = __all_sync(0xffffffffu, mbar_wait(gu_empty, (tc - 1) & 1, abort_flag));
-        if (ph == 1 && tc >= 2)
-          ok = __all_sync(0xffffffffu, mbar_wait(&dh_empty[buf], ((tc >> 1) - 1) & 1, abort_flag));
-        if (!ok) {
-          if (lane == 0) { *abort_flag = 1; report_error(a.status, MOE_ERR_TIMEOUT, 62); }
-          break;
-        }
-        tc_fence_after();
-        const uint32_t idesc = instr_desc(a.bf16, 0, ph, T::BM, ph ? NI : 2 * NI);
-        const uint32_t d = tmem + (ph ? uint32_t(2 * NI + buf * NI) : 0u);
-        for (int kb = 0; kb < a.kblocks; ++kb, ++kc) {
-          const int s = kc % T::STAGES;
-          ok = __all_sync(0xffffffffu, mbar_wait(&full[s], (kc / T::STAGES) & 1, abort_flag));
-          if (!ok) {
-            if (lane == 0) { *abort_flag = 1; report_error(a.status, MOE_ERR_TIMEOUT, 63); }
-            break;
-          }
-          tc_fence_after();
-          const uint32_t sa = smem_u32(base + size_t(s) * T::STAGE);
-          if (elect_one()) {
-            mma_stage<CG>(d, sa, sa + kAStage, 0, ph, idesc, kb == 0);
-            commit<CG>(&empty[s]);
-            if (kb == a.kblocks - 1) commit<CG>(ph ? &dh_full[buf] : gu_full);
-          }
-          __syncwarp();
-        }
-      }
+      ok = __all_sync(0xffffffffu, mbar_wait(gu_empty, (tc & 1) ^ 1, abort_flag));
+      if (!ok) break;
+      tc_fence_after();
+      ok = mma_steps<CG, false, false, T::STAGE, T::STAGES>(ring, full, empty, c, tmem, id_gu, a.kblocks, gu_full, abort_flag);
+      if (!ok) break;
+      ok = __all_sync(0xffffffffu, mbar_wait(&dh_empty[buf], ((tc >> 1) & 1) ^ 1, abort_flag));
+      if (!ok) break;
+      tc_fence_after();
+      ok = mma_steps<CG, false, true, T::STAGE, T::STAGES>(ring, full, empty, c, tmem + uint32_t(2 * NI + buf * NI), id_dh,
+                                                          a.kblocks, &dh_full[buf], abort_flag);
     }
+    if (!ok && lane == 0) { *abort_flag = 1; report_error(a.status, MOE_ERR_TIMEOUT, 62); }
   } else if (warp < kGradEpi) {
     const int q = warp & 3, part = warp >> 2;
     constexpr int PI = NI / 4;                    // hidden elements of this thread
