@@ -251,16 +251,27 @@ __device__ __forceinline__ uint32_t pack2(float a, float b, int bf16) {
   }
   return h2_as_u32(__floats2half2_rn(a, b));
 }
-// NV values of a row from column n (NV and the row's column count are
-// multiples of 8): 16-byte stores of the part inside the row.
-template <int NV>
-__device__ __forceinline__ void store_row(uint16_t* row, int n, int cols, const float (&v)[NV], int bf16) {
+// 16 values of a row from column n (n a multiple of 16, the row's column count
+// of 8): one 32-byte store where the row starts on 32 bytes, so that a thread
+// always writes whole sectors (16-byte stores of 32 different rows per
+// instruction reach L2 as two writes a sector), else 16-byte stores of the part
+// inside the row.
+__device__ __forceinline__ void store16(uint16_t* row, int n, int cols, const float (&v)[16], int bf16, bool wide) {
+  uint32_t w[8];
 #pragma unroll
-  for (int i = 0; i < NV; i += 8)
-    if (n + i < cols)
-      *reinterpret_cast<uint4*>(row + n + i) =
-          make_uint4(pack2(v[i], v[i + 1], bf16), pack2(v[i + 2], v[i + 3], bf16), pack2(v[i + 4], v[i + 5], bf16),
-                     pack2(v[i + 6], v[i + 7], bf16));
+  for (int i = 0; i < 8; ++i) w[i] = pack2(v[2 * i], v[2 * i + 1], bf16);
+  if (wide && n + 16 <= cols) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(row + n), "r"(w[0]), "r"(w[1]),
+                 "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+  } else {
+    if (n < cols) *reinterpret_cast<uint4*>(row + n) = make_uint4(w[0], w[1], w[2], w[3]);
+    if (n + 8 < cols) *reinterpret_cast<uint4*>(row + n + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+  }
+}
+// All rows of [][ld] start on 32 bytes.
+__device__ __forceinline__ bool on_32(const void* p, int ld) {
+  return (reinterpret_cast<uintptr_t>(p) & 31) == 0 && (ld & 15) == 0;
 }
 __device__ __forceinline__ float sigmoid(float g) { return __fdividef(1.f, 1.f + __expf(-g)); }
 
@@ -380,6 +391,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ffn_gemm_kernel(const __grid_
       const int row = m * T::BM + rank * 128 + q * 32 + lane;
       const uint32_t tq = tmem + (uint32_t(q * 32) << 16) + uint32_t(buf * BN + half * HC);
       uint16_t* out = static_cast<uint16_t*>(p.out) + size_t(row) * p.ld;
+      const bool wide = on_32(p.out, p.ld);
 #pragma unroll
       for (int c = 0; c < HC; c += 32) {
         uint32_t v[32];
@@ -387,10 +399,13 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ffn_gemm_kernel(const __grid_
         const int col = n * BN + half * HC + c;
         if (row < p.M) {
           if (EPI == EPI_STORE) {
-            float f[32];
 #pragma unroll
-            for (int j = 0; j < 32; ++j) f[j] = __uint_as_float(v[j]);
-            store_row<32>(out, col, p.ld, f, a.bf16);
+            for (int e = 0; e < 32; e += 16) {
+              float f[16];
+#pragma unroll
+              for (int j = 0; j < 16; ++j) f[j] = __uint_as_float(v[e + j]);
+              store16(out, col + e, p.ld, f, a.bf16, wide);
+            }
           } else {
             float f[16];
 #pragma unroll
@@ -398,7 +413,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ffn_gemm_kernel(const __grid_
               const float g = __uint_as_float(v[2 * j]), u = __uint_as_float(v[2 * j + 1]);
               f[j] = g * sigmoid(g) * u;
             }
-            store_row<16>(out, col >> 1, p.ld, f, a.bf16);
+            store16(out, col >> 1, p.ld, f, a.bf16, wide);
           }
         }
       }
@@ -524,6 +539,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) ffn_grad_kernel(const __grid_
   } else if (warp < kGradEpi) {
     const int q = warp & 3, part = warp >> 2;
     constexpr int PI = NI / 4;                    // hidden elements of this thread
+    const bool h_wide = on_32(a.h, a.I), dgu_wide = on_32(a.dgu, 2 * a.I);
     int tc = 0;
     for (int t = unit; t < ntiles; t += units, ++tc) {
       int m, n;
@@ -540,19 +556,22 @@ __global__ void __launch_bounds__(kGradThreads, 1) ffn_grad_kernel(const __grid_
       tc_fence_after();
       float fg[PI], fu[PI];
 #pragma unroll
-      for (int c = 0; c < PI; c += 8) {
-        uint32_t v[16];
-        tmem_ld16(tq + uint32_t(2 * (part * PI + c)), v);
-        float hv[8];
+      for (int c = 0; c < PI; c += 16) {
+        float hv[16];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float g = __uint_as_float(v[2 * j]), u = __uint_as_float(v[2 * j + 1]);
-          const float s = sigmoid(g), act = g * s;
-          hv[j] = act * u;
-          fu[c + j] = act;
-          fg[c + j] = u * fmaf(act, 1.f - s, s);
+        for (int e = 0; e < 16; e += 8) {
+          uint32_t v[16];
+          tmem_ld16(tq + uint32_t(2 * (part * PI + c + e)), v);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float g = __uint_as_float(v[2 * j]), u = __uint_as_float(v[2 * j + 1]);
+            const float s = sigmoid(g), act = g * s;
+            hv[e + j] = act * u;
+            fu[c + e + j] = act;
+            fg[c + e + j] = u * fmaf(act, 1.f - s, s);
+          }
         }
-        if (a.h && row < a.T) store_row<8>(a.h + size_t(row) * a.I, i0 + c, a.I, hv, a.bf16);
+        if (a.h && row < a.T) store16(a.h + size_t(row) * a.I, i0 + c, a.I, hv, a.bf16, h_wide);
       }
       tc_fence_before();
       __syncwarp();
@@ -569,15 +588,15 @@ __global__ void __launch_bounds__(kGradThreads, 1) ffn_grad_kernel(const __grid_
         tmem_ld16(tq + uint32_t(2 * NI + buf * NI + part * PI + c), v);
         if (row < a.T) {
 #pragma unroll
-          for (int e = 0; e < 16; e += 4) {
-            float d[8];
+          for (int e = 0; e < 16; e += 8) {
+            float d[16];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
+            for (int j = 0; j < 8; ++j) {
               const float dh = __uint_as_float(v[e + j]);
               d[2 * j] = dh * fg[c + e + j];
               d[2 * j + 1] = dh * fu[c + e + j];
             }
-            store_row<8>(a.dgu + size_t(row) * 2 * a.I, 2 * (i0 + c + e), 2 * a.I, d, a.bf16);
+            store16(a.dgu + size_t(row) * 2 * a.I, 2 * (i0 + c + e), 2 * a.I, d, a.bf16, dgu_wide);
           }
         }
       }
