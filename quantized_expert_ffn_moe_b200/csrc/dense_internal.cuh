@@ -50,6 +50,29 @@ cudaError_t launch_ffn_backward(const FfnCall& c, int num_sms, cudaStream_t s);
 int num_sms_of_current_device();
 int status_of_cuda(cudaError_t e);
 
+// launch_pdl with clusters of cg CTAs.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_cluster(void (*kernel)(KArgs...), int cg, int grid, int threads, size_t smem, cudaStream_t s,
+                           const Args&... args) {
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = unsigned(cg);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cg > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // One value rounded to a moe_type and stored at index `at`.
 __device__ __forceinline__ void store_as(void* p, int type, size_t at, float v) {
   if (type == MOE_FP32) static_cast<float*>(p)[at] = v;

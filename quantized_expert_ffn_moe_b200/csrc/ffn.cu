@@ -625,28 +625,6 @@ bool operand_map(CUtensorMap* m, int bf16, const void* p, int rows, int cols, in
                   uint64_t(rows), BK, mn ? 64 : uint32_t(box_rows), CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-template <typename... KArgs, typename... Args>
-cudaError_t launch_cluster(void (*kernel)(KArgs...), int cg, int grid, int threads, size_t smem, cudaStream_t s,
-                           const Args&... args) {
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
-  if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = unsigned(cg);
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = cg > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
 // One operand pair of a launch: matrices as stored.
 struct Operands {
   const void* a; int a_rows, a_cols;

@@ -30,7 +30,11 @@
 // private ring of asynchronous copies (no block-wide barrier in the stream);
 // the warps of a group split the columns of a row tile, so that even 2048 x
 // 2048 spreads over 128 SMs, and join their fp32 sums through shared memory in
-// a fixed order: the same inputs give the same bits.
+// a fixed order: the same inputs give the same bits.  With many tokens the
+// CTAs of a cluster split the columns too: each converts and keeps the
+// activations of its columns alone, every code is dequantised once for all of
+// up to 64 tokens, and the tile's sums are joined over distributed shared
+// memory while the next tile's stages are multiplied.
 #include "dense_internal.cuh"
 
 namespace moe {
@@ -73,6 +77,7 @@ struct LinearArgs {
   int nb;               // 32-element blocks of a row
   int spr;              // scales of a row
   int chunks;           // stages of a row
+  int C, cpr;           // CTAs of a cluster, stages of a row that each takes
   int KG, groups;       // warps splitting a row tile's columns; row tiles in flight per CTA
   int ny, tt;           // token slices, tokens of a slice
   int x_type, y_type, gated;
@@ -153,11 +158,29 @@ __device__ __forceinline__ void stage_scales(const unsigned char* sc, int row, f
   }
 }
 
-// Shared memory: ring | x [tt][nb | 1][4] 16-byte words (an odd number of
-// blocks, so that two tokens' words fall into different banks) | partial sums [groups
-// KG][16][8 NT] floats | inv [8 NT] floats | row maxima [tt][16] u32.
-inline size_t linear_smem(int ring, int nb, int tt, int nt) {
-  return size_t(ring) + size_t(nb | 1) * tt * 64 + size_t(kWarps) * 16 * 8 * nt * 4 + size_t(nt) * 32 + size_t(tt) * 64;
+// Shared memory: ring | x [tt][xblocks][4] 16-byte words | sums of the warps
+// that join another's [groups (KG - 1)][NT][32 lanes] float4 | (C > 1) a tile's
+// sums for the cluster, two rounds [groups][NT][32] float4 | inv [8 NT] floats |
+// row maxima [tt][16] u32.  xblocks is odd, so that two tokens' words fall into
+// different banks.
+__host__ __device__ inline int x_blocks(int cpr, int CB) { return (cpr * CB) | 1; }
+__host__ __device__ inline int join_bytes(int groups, int KG, int NT) { return groups * (KG - 1) * NT * 512; }
+__host__ __device__ inline int cluster_bytes(int groups, int C, int NT) { return C > 1 ? 2 * groups * NT * 512 : 0; }
+inline size_t linear_smem(int ring, int CB, int cpr, int tt, int NT, int groups, int KG, int C) {
+  return size_t(ring) + size_t(x_blocks(cpr, CB)) * tt * 64 + join_bytes(groups, KG, NT) +
+         cluster_bytes(groups, C, NT) + size_t(NT) * 32 + size_t(tt) * 64;
+}
+
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+// A float4 of CTA `rank`'s copy of a shared-memory location.
+__device__ __forceinline__ float4 ld_cluster(const void* p, int rank) {
+  uint32_t a;
+  float4 v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a)
+               : "memory");
+  return v;
 }
 
 // Eight activations as fp16 pairs (j, j + 4), the order of `levels`.
@@ -189,21 +212,23 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const LinearArgs a)
   const int warp = __shfl_sync(0xffffffffu, int(threadIdx.x) >> 5, 0), lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
   const int nb = a.nb, tt = a.tt;
-  constexpr int TP = 8 * NT;
+  const int xpitch = x_blocks(a.cpr, CB) * 64;
   unsigned char* sx = lsm + S::RING;
-  float* spart = reinterpret_cast<float*>(sx + (nb | 1) * tt * 64);
-  float* sinv = spart + kWarps * 16 * TP;
-  uint32_t* smax = reinterpret_cast<uint32_t*>(sinv + TP);
+  unsigned char* sjoin = sx + xpitch * tt;
+  unsigned char* sout = sjoin + join_bytes(a.groups, a.KG, NT);
+  float* sinv = reinterpret_cast<float*>(sout + cluster_bytes(a.groups, a.C, NT));
+  uint32_t* smax = reinterpret_cast<uint32_t*>(sinv + 8 * NT);
 
-  const int xpitch = (nb | 1) * 64;
-  const int slice = int(blockIdx.x % unsigned(a.ny)), cta = int(blockIdx.x / unsigned(a.ny));
-  const int ctas = int(gridDim.x / unsigned(a.ny));
+  const int rank = int(blockIdx.x % unsigned(a.C)), unit = int(blockIdx.x / unsigned(a.C));
+  const int slice = unit % a.ny, cta = unit / a.ny, ctas = int(gridDim.x / unsigned(a.C * a.ny));
   const int t0 = slice * tt, nt = min(tt, a.T - t0);     // this CTA's tokens
+  const int c_lo = rank * a.cpr, c_hi = min(c_lo + a.cpr, a.chunks);     // and stages of a row
   const int ntiles = (a.N + 15) >> 4;
   const int grp = warp / a.KG, kw = warp - grp * a.KG;
   // neighbouring tiles go to different CTAs, so that CTAs differ by one tile at most
   const int first = grp * ctas + cta, step = ctas * a.groups;
-  const int my_chunks = grp < a.groups ? (a.chunks - kw + a.KG - 1) / a.KG : 0;
+  const int rounds = (ntiles - cta + step - 1) / step;   // of group 0: the most of any
+  const int my_chunks = grp < a.groups ? (c_hi - c_lo - kw + a.KG - 1) / a.KG : 0;
   const int my_tiles = grp < a.groups && first < ntiles ? (ntiles - first + step - 1) / step : 0;
   const int total = my_tiles * my_chunks;
 
@@ -250,14 +275,14 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const LinearArgs a)
     dst_off[i] = r * S::ROW + ((ch ^ (CB == 8 ? r & 7 : (r >> 1) & 3)) << 4);
   }
   auto enter_tile = [&]() {
-    it_chunk = kw;
+    it_chunk = c_lo + kw;
     if (it_tile * 16 + 16 > a.N) {
 #pragma unroll
       for (int i = 0; i < CB / 2; ++i) row_off[i] = min(i * RS, a.N - 1 - it_tile * 16 - r0) * row_bytes;
     }
-    src = a.codes + size_t(it_tile * 16 + r0) * row_bytes + size_t(kw) * S::ROW + ch * 16;
+    src = a.codes + size_t(it_tile * 16 + r0) * row_bytes + size_t(it_chunk) * S::ROW + ch * 16;
     ssrc = static_cast<const uint8_t*>(a.scales) +
-           (size_t(min(it_tile * 16 + (lane & 15), a.N - 1)) * a.spr + size_t(kw) * SPC) * F::SB;
+           (size_t(min(it_tile * 16 + (lane & 15), a.N - 1)) * a.spr + size_t(it_chunk) * SPC) * F::SB;
   };
   if (left > 0) enter_tile();
   auto issue = [&]() {
@@ -292,7 +317,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const LinearArgs a)
       it_chunk += a.KG;
       src += a.KG * S::ROW;
       ssrc += a.KG * SPC * F::SB;
-      if (it_chunk >= a.chunks) {
+      if (it_chunk >= c_hi) {
         it_tile += step;
         if (left > 0) enter_tile();
       }
@@ -314,10 +339,11 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const LinearArgs a)
     constexpr int HOLD = 8;
     const int sl = nt >= kWarps ? 1 : kWarps / nt;         // slices of a token
     const int units = nt * sl;
-    const int K8 = a.K >> 3;                               // 16-byte words of a token row
+    const int col0 = c_lo * CB * 32;
+    const int K8 = min(c_hi * CB * 32, a.K) - col0 >> 3;   // 16-byte words of this CTA's columns
     const int per = (K8 + sl - 1) / sl;
     const bool bf = a.x_type == MOE_BF16;
-    const uint16_t* xb = static_cast<const uint16_t*>(a.x) + size_t(t0) * a.K;
+    const uint16_t* xb = static_cast<const uint16_t*>(a.x) + size_t(t0) * a.K + col0;
     const bool held = units <= kWarps && per <= HOLD * 32;
     uint4 hold[HOLD];
     auto word_max = [](uint32_t m, const uint4& v) {
@@ -375,7 +401,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const LinearArgs a)
     }
     __syncthreads();
   }
-  if (total == 0) return;             // whole warps; a group's warps leave together
+  if (a.C == 1 && my_tiles == 0) return;     // whole groups of warps
 
   // ------------------------------------------------------------ stream
   // this lane's words of the tokens 8 j + g (the last token's where there is
@@ -390,133 +416,271 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const LinearArgs a)
 #pragma unroll
     for (int i = 0; i < 4; ++i) acc[j][i] = 0.f;
 
-  int tile = first, chunk = kw, slot = 0;
-  bool first_tile = true;
-  for (int it = 0; it < total; ++it) {
-    __syncwarp();                     // every lane is done with the slot that is filled next
-    issue();
-    cp_async_wait<S::ST - 1>();
-    __syncwarp();
-    const unsigned char* st = ring + slot * S::BYTES;
-    slot = slot + 1 == S::ST ? 0 : slot + 1;
-    float s0[CB], s1[CB];
-    stage_scales<FMT, CB>(st + S::CODES, g, s0);
-    stage_scales<FMT, CB>(st + S::CODES, g + 8, s1);
-    const int nblk = min(CB, nb - chunk * CB);
-    // rows g and g + 8 share the swizzle; a stage's offset is a multiple of 128
-    const uint32_t code0 = uint32_t(st - lsm) + lane_code;
-    const unsigned char* xc[NT];
+  // The results of 16 rows and 8 tokens in the instruction's layout: rows g
+  // and g + 8, tokens 8 j + 2 t and + 1.
+  auto finish = [&](float4 v, int tile, int j) {
+    const int row = tile * 16 + g, n = 8 * j + 2 * t;
+    if (FMT == F_E32) {
+      const float r0 = __ldg(a.row_scales + min(row, a.N - 1)), r1 = __ldg(a.row_scales + min(row + 8, a.N - 1));
+      v.x *= r0; v.y *= r0; v.z *= r1; v.w *= r1;
+    }
+    if (!a.gated) {
+      if (a.bias) {
+        const float b0 = __ldg(a.bias + min(row, a.N - 1)), b1 = __ldg(a.bias + min(row + 8, a.N - 1));
+        v.x += b0; v.y += b0; v.z += b1; v.w += b1;
+      }
+      const size_t at = size_t(t0 + n) * a.N + row;
+      if (n < nt) {
+        if (row < a.N) store_as(a.y, a.y_type, at, v.x);
+        if (row + 8 < a.N) store_as(a.y, a.y_type, at + 8, v.z);
+      }
+      if (n + 1 < nt) {
+        if (row < a.N) store_as(a.y, a.y_type, at + a.N, v.y);
+        if (row + 8 < a.N) store_as(a.y, a.y_type, at + a.N + 8, v.w);
+      }
+    } else {
+      // even g holds a gate row, odd g its up row: the even lane takes the
+      // first token of the pair, the odd lane the second
+      const bool odd = g & 1;
+      const float o0 = __shfl_xor_sync(0xffffffffu, odd ? v.x : v.y, 4);
+      const float o1 = __shfl_xor_sync(0xffffffffu, odd ? v.z : v.w, 4);
+      const float g0 = odd ? o0 : v.x, u0 = odd ? v.y : o0, g1 = odd ? o1 : v.z, u1 = odd ? v.w : o1;
+      const int m = n + (odd ? 1 : 0), out = a.N >> 1, i = row >> 1;
+      if (m < nt) {
+        const size_t at = size_t(t0 + m) * out + i;
+        if (i < out) store_as(a.y, a.y_type, at, g0 / (1.f + expf(-g0)) * u0);
+        if (i + 4 < out) store_as(a.y, a.y_type, at + 4, g1 / (1.f + expf(-g1)) * u1);
+      }
+    }
+  };
+  // A round's sums of all CTAs of the cluster, added by rank; the 8-token
+  // groups of its tiles are dealt to the ranks and their warps.
+  auto join_cluster = [&](int round) {
+    const unsigned char* buf = sout + (round & 1) * (a.groups * NT * 512);
+    for (int id = rank + a.C * warp; id < a.groups * NT; id += a.C * kWarps) {
+      const int gi = id / NT, tile = gi * ctas + cta + round * step;
+      if (tile >= ntiles) continue;
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int q = 0; q < a.C; ++q) {
+        const float4 o = ld_cluster(buf + id * 512 + lane * 16, q);
+        v.x += o.x; v.y += o.y; v.z += o.z; v.w += o.w;
+      }
+      finish(v, tile, id - gi * NT);
+    }
+  };
+  auto group_sync = [&]() { named_bar_sync(1 + grp, a.KG * 32); };
+
+  int slot = 0;
+  for (int round = 0; round < rounds; ++round) {
+    const int tile = first + round * step;
+    const bool has = round < my_tiles;
+    if (has) {
+      for (int chunk = c_lo + kw; chunk < c_hi; chunk += a.KG) {
+        __syncwarp();                 // every lane is done with the slot that is filled next
+        issue();
+        cp_async_wait<S::ST - 1>();
+        __syncwarp();
+        const unsigned char* st = ring + slot * S::BYTES;
+        slot = slot + 1 == S::ST ? 0 : slot + 1;
+        float s0[CB], s1[CB];
+        stage_scales<FMT, CB>(st + S::CODES, g, s0);
+        stage_scales<FMT, CB>(st + S::CODES, g + 8, s1);
+        const int nblk = min(CB, nb - chunk * CB);
+        // rows g and g + 8 share the swizzle; a stage's offset is a multiple of 128
+        const uint32_t code0 = uint32_t(st - lsm) + lane_code;
+        const int xc = (chunk - c_lo) * (CB * 64);
+        // one scale for a whole stage of 4 blocks: their sums chain in the
+        // instruction (not with 64 tokens: the chains' registers would spill)
+        constexpr bool kChain = F::G128 && NT < 8;
+        float d[kChain ? NT : 1][4];
+        // fold: the sums so far take the scale of block b
+        auto block = [&](int b, bool start, bool fold) {
+          uint32_t q0[4], q1[4];
+          levels<F::HALF>(*reinterpret_cast<const uint32_t*>(lsm + (code0 ^ (b << 4))), q0);
+          levels<F::HALF>(*reinterpret_cast<const uint32_t*>(lsm + (code0 ^ (b << 4)) + 8 * S::ROW), q1);
+          const uint32_t lo[4] = {q0[0], q1[0], q0[1], q1[1]}, hi[4] = {q0[2], q1[2], q0[3], q1[3]};
 #pragma unroll
-    for (int j = 0; j < NT; ++j) xc[j] = xrow[j] + chunk * (CB * 64);
-    float d[NT][4];
-    // fold: the sums so far take the scale of block b
-    auto block = [&](int b, bool start, bool fold) {
-      uint32_t q0[4], q1[4];
-      levels<F::HALF>(*reinterpret_cast<const uint32_t*>(lsm + (code0 ^ (b << 4))), q0);
-      levels<F::HALF>(*reinterpret_cast<const uint32_t*>(lsm + (code0 ^ (b << 4)) + 8 * S::ROW), q1);
-      const uint32_t lo[4] = {q0[0], q1[0], q0[1], q1[1]}, hi[4] = {q0[2], q1[2], q0[3], q1[3]};
+          for (int j = 0; j < NT; ++j) {
+            const uint4 xv = *reinterpret_cast<const uint4*>(xrow[j] + xc + b * 64);
+            float (&dj)[4] = d[kChain ? j : 0];
+            if (start) mma16816(dj, lo, xv.x, xv.y, 0.f, 0.f, 0.f, 0.f);
+            else mma16816(dj, lo, xv.x, xv.y, dj[0], dj[1], dj[2], dj[3]);
+            mma16816(dj, hi, xv.z, xv.w, dj[0], dj[1], dj[2], dj[3]);
+            if (fold) {
+              acc[j][0] = fmaf(s0[b], dj[0], acc[j][0]);
+              acc[j][1] = fmaf(s0[b], dj[1], acc[j][1]);
+              acc[j][2] = fmaf(s1[b], dj[2], acc[j][2]);
+              acc[j][3] = fmaf(s1[b], dj[3], acc[j][3]);
+            }
+          }
+        };
+        if (nblk == CB) {
 #pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        const uint4 xv = *reinterpret_cast<const uint4*>(xc[j] + b * 64);
-        if (start) mma16816(d[j], lo, xv.x, xv.y, 0.f, 0.f, 0.f, 0.f);
-        else mma16816(d[j], lo, xv.x, xv.y, d[j][0], d[j][1], d[j][2], d[j][3]);
-        mma16816(d[j], hi, xv.z, xv.w, d[j][0], d[j][1], d[j][2], d[j][3]);
-        if (fold) {
-          acc[j][0] = fmaf(s0[b], d[j][0], acc[j][0]);
-          acc[j][1] = fmaf(s0[b], d[j][1], acc[j][1]);
-          acc[j][2] = fmaf(s1[b], d[j][2], acc[j][2]);
-          acc[j][3] = fmaf(s1[b], d[j][3], acc[j][3]);
+          for (int b = 0; b < CB; ++b) block(b, !kChain || (b & 3) == 0, !kChain || (b & 3) == 3);
+        } else {
+#pragma unroll
+          for (int b = 0; b < CB - 1; ++b)
+            if (b < nblk) block(b, !kChain || (b & 3) == 0, !kChain || (b & 3) == 3);
         }
       }
-    };
-    if (nblk == CB) {
-#pragma unroll
-      for (int b = 0; b < CB; ++b) block(b, !F::G128 || (b & 3) == 0, !F::G128 || (b & 3) == 3);
-    } else {
-#pragma unroll
-      for (int b = 0; b < CB - 1; ++b)
-        if (b < nblk) block(b, !F::G128 || (b & 3) == 0, !F::G128 || (b & 3) == 3);
     }
-    chunk += a.KG;
-    if (chunk < a.chunks) continue;
-
-    // ---------------------------------------------- the tile's epilogue
-    const int bar = 1 + grp, bar_n = a.KG * 32;
-    auto group_sync = [&]() {
-      if (a.KG > 1) named_bar_sync(bar, bar_n);
-      else __syncwarp();
-    };
-    if (!first_tile) group_sync();    // the previous tile's sums have been read
-    first_tile = false;
-    float* gp = spart + size_t(grp) * a.KG * 16 * TP;
-#pragma unroll
-    for (int j = 0; j < NT; ++j) {
-      float* p = gp + (kw * 16 + g) * TP + 8 * j + 2 * t;
-      *reinterpret_cast<float2*>(p) = make_float2(acc[j][0], acc[j][1]);
-      *reinterpret_cast<float2*>(p + 8 * TP) = make_float2(acc[j][2], acc[j][3]);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) acc[j][i] = 0.f;
+    if (a.C > 1 && round > 0) {       // the round before: its sums have had this round's time to arrive
+      __syncwarp();
+      cluster_wait();
+      join_cluster(round - 1);
     }
-    group_sync();
-    const int row0 = tile * 16, tid = kw * 32 + lane;
-    auto sum_of = [&](int row, int n) {
-      const float* p = gp + row * TP + n;
-      float v = 0.f;
-#pragma unroll 4
-      for (int w = 0; w < a.KG; ++w) v += p[w * 16 * TP];
-      v *= sinv[n];
-      if (FMT == F_E32) v *= __ldg(a.row_scales + row0 + row);
-      return v;
-    };
-    if (!a.gated) {
-      for (int o = tid; o < 16 * nt; o += bar_n) {
-        const int row = o & 15, n = o >> 4;
-        if (row0 + row >= a.N) continue;
-        float v = sum_of(row, n);
-        if (a.bias) v += __ldg(a.bias + row0 + row);
-        store_as(a.y, a.y_type, size_t(t0 + n) * a.N + row0 + row, v);
+    if (has) {
+      if (a.KG > 1) {
+        float4* j0 = reinterpret_cast<float4*>(sjoin) + grp * (a.KG - 1) * NT * 32 + lane;
+        if (round > 0) group_sync();  // the last tile's sums have been read
+        if (kw > 0) {
+#pragma unroll
+          for (int j = 0; j < NT; ++j)
+            j0[((kw - 1) * NT + j) * 32] = make_float4(acc[j][0], acc[j][1], acc[j][2], acc[j][3]);
+        }
+        group_sync();
+        if (kw == 0) {
+          for (int w = 0; w < a.KG - 1; ++w)
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+              const float4 o = j0[(w * NT + j) * 32];
+              acc[j][0] += o.x; acc[j][1] += o.y; acc[j][2] += o.z; acc[j][3] += o.w;
+            }
+        }
       }
-    } else {
-      for (int o = tid; o < 8 * nt; o += bar_n) {
-        const int i = o & 7, n = o >> 3;
-        if (row0 + 2 * i >= a.N) continue;
-        const float gt = sum_of(2 * i, n), up = sum_of(2 * i + 1, n);
-        store_as(a.y, a.y_type, size_t(t0 + n) * (a.N >> 1) + (row0 >> 1) + i, gt / (1.f + expf(-gt)) * up);
+      if (kw == 0) {
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          const float i0 = sinv[8 * j + 2 * t], i1 = sinv[8 * j + 2 * t + 1];
+          const float4 v = make_float4(acc[j][0] * i0, acc[j][1] * i1, acc[j][2] * i0, acc[j][3] * i1);
+          if (a.C == 1) finish(v, tile, j);
+          else reinterpret_cast<float4*>(sout)[((round & 1) * a.groups * NT + grp * NT + j) * 32 + lane] = v;
+        }
       }
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[j][i] = 0.f;
     }
-    chunk = kw;
-    tile += step;
+    if (a.C > 1) {
+      __syncwarp();
+      cluster_arrive();
+    }
+  }
+  if (a.C > 1) {
+    cluster_wait();
+    join_cluster(rounds - 1);
+    __syncwarp();
+    cluster_arrive();                 // no CTA leaves while another reads its sums
+    cluster_wait();
   }
   cp_async_wait<0>();
 }
 
-template <int FMT, int CB>
-cudaError_t launch_fmt(const LinearArgs& a, int nt, int grid, size_t smem, cudaStream_t s) {
-  auto kern = nt == 1 ? linear_kernel<1, FMT, CB> : nt == 2 ? linear_kernel<2, FMT, CB> : linear_kernel<4, FMT, CB>;
+template <int NT, int FMT, int CB>
+cudaError_t launch_kernel(const LinearArgs& a, int grid, size_t smem, cudaStream_t s) {
+  auto kern = linear_kernel<NT, FMT, CB>;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
   if (e != cudaSuccess) return e;
-  return launch_pdl(kern, dim3(grid), dim3(kThreads), smem, s, a);
+  return a.C == 1 ? launch_pdl(kern, dim3(grid), dim3(kThreads), smem, s, a)
+                  : launch_cluster(kern, a.C, grid, kThreads, smem, s, a);
 }
 
-template <int CB>
-cudaError_t launch_stage(int fmt, const LinearArgs& a, int nt, int grid, size_t smem, cudaStream_t s) {
+template <int NT, int CB>
+cudaError_t launch_fmt(int fmt, const LinearArgs& a, int grid, size_t smem, cudaStream_t s) {
   switch (fmt) {
-    case F_H32: return launch_fmt<F_H32, CB>(a, nt, grid, smem, s);
-    case F_H128: return launch_fmt<F_H128, CB>(a, nt, grid, smem, s);
-    case F_E32: return launch_fmt<F_E32, CB>(a, nt, grid, smem, s);
-    case F_H32_HALF: return launch_fmt<F_H32_HALF, CB>(a, nt, grid, smem, s);
-    default: return launch_fmt<F_H128_HALF, CB>(a, nt, grid, smem, s);
+    case F_H32: return launch_kernel<NT, F_H32, CB>(a, grid, smem, s);
+    case F_H128: return launch_kernel<NT, F_H128, CB>(a, grid, smem, s);
+    case F_E32: return launch_kernel<NT, F_E32, CB>(a, grid, smem, s);
+    case F_H32_HALF: return launch_kernel<NT, F_H32_HALF, CB>(a, grid, smem, s);
+    default: return launch_kernel<NT, F_H128_HALF, CB>(a, grid, smem, s);
   }
 }
 
-int groups_of_8(int tt) { return tt <= 8 ? 1 : tt <= 16 ? 2 : 4; }
+int groups_of_8(int tt) { return tt <= 8 ? 1 : tt <= 16 ? 2 : tt <= 32 ? 4 : 8; }
 
-// The most tokens (up to 32) whose activations fit beside a ring.
-int most_tokens(int ring, int nb) {
-  int most = 0;
-  for (int tt = 1; tt <= 32; ++tt)
-    if (linear_smem(ring, nb, tt, groups_of_8(tt)) <= kMaxSmem) most = tt;
-  return most;
+// Clusters of C CTAs with a full SM each that run at once on this device.
+int clusters_at_once(int C, int num_sms) {
+  static int cached[64][4] = {};
+  if (C == 1) return num_sms;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return num_sms / 8 * 8 / C;
+  int& n = cached[dev][C == 2 ? 1 : C == 4 ? 2 : 3];
+  if (n == 0) {
+    auto kern = linear_kernel<1, F_H32, 4>;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(num_sms / C * C);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = 200 * 1024;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = unsigned(C);
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int got = 0;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&got, kern, &cfg) != cudaSuccess || got <= 0) {
+      (void)cudaGetLastError();
+      got = max(1, num_sms / 8 * 8 / C);
+    }
+    n = got;
+  }
+  return n;
+}
+
+struct Plan {
+  int C, CB, cpr, chunks, KG, groups, tt, ny, ctas;
+  size_t smem;
+  double cost;
+};
+
+// The launch that ends first by a rough count of cycles (fitted to measured
+// calls): converting a CTA's activations, its share of the blocks at the rate
+// the warps' instructions issue (38 + 9 for each 8 tokens, 2.5 a cycle), or a
+// warp's own chain of stages where there are few.
+Plan plan_linear(int N, int nb, int T, int num_sms) {
+  Plan best{};
+  best.cost = -1;
+  const int tiles = (N + 15) / 16;
+  for (int C = 1; C <= 8; C *= 2) {
+    const int at_once = clusters_at_once(C, num_sms);
+    for (int CB = 8; CB >= 4; CB -= 4) {
+      Plan p{};
+      p.C = C; p.CB = CB;
+      p.chunks = (nb + CB - 1) / CB;
+      p.cpr = (p.chunks + C - 1) / C;
+      if (C > 1 && (C - 1) * p.cpr >= p.chunks) continue;      // a rank without columns
+      const int ring = CB == 8 ? Stage<8>::RING : Stage<4>::RING;
+      for (int KG = 1; KG <= kWarps; KG *= 2) {
+        if (KG > p.cpr && KG > 1) break;
+        p.KG = KG;
+        // the most tokens (up to 64) that fit, then as few slices as that takes
+        const int gmax = min(kWarps / KG, tiles);
+        int most = 0;
+        for (int NT = groups_of_8(T); NT >= 1 && most == 0; NT /= 2) {
+          const size_t fixed = linear_smem(ring, CB, p.cpr, 0, NT, gmax, KG, C);
+          const int fit = fixed >= kMaxSmem ? 0 : int((kMaxSmem - fixed) / (size_t(x_blocks(p.cpr, CB)) * 64 + 64));
+          if (fit > 4 * NT || (NT == 1 && fit > 0)) most = min(min(fit, 8 * NT), T);
+        }
+        if (most == 0) continue;
+        p.ny = (T + most - 1) / most;
+        p.tt = (T + p.ny - 1) / p.ny;
+        const int sms = max(1, at_once / p.ny);
+        p.groups = min(gmax, (tiles + sms - 1) / sms);
+        p.ctas = min((tiles + p.groups - 1) / p.groups, sms);
+        p.smem = linear_smem(ring, CB, p.cpr, p.tt, groups_of_8(p.tt), p.groups, KG, C);
+        const int NT = groups_of_8(p.tt), per = (tiles + p.ctas - 1) / p.ctas, waves = (p.ny * p.ctas + at_once - 1) / at_once;
+        const int rounds = (per + p.groups - 1) / p.groups, stages = (p.cpr + KG - 1) / KG;
+        const double block = (38 + 9 * NT) / 2.5, stage = 200 + CB * (20 + 6 * NT);
+        const double thr = per * (double(p.cpr) * CB * block + 60 + KG * (10 + 4 * NT));
+        const double lat = rounds * (stages * stage + 200 + (C > 1 ? 100 : 0));
+        p.cost = waves * (1000 + p.tt * double(p.cpr) * CB * 32 * 0.08 + (C > 1 ? 1500 : 0) + (thr > lat ? thr : lat));
+        if (best.cost < 0 || p.cost < best.cost) best = p;
+      }
+    }
+  }
+  return best;
 }
 
 }  // namespace
@@ -531,37 +695,26 @@ cudaError_t launch_linear(const LinearCall& c, int num_sms, cudaStream_t s) {
   const int fmt = c.scale_fmt == 1 ? F_E32
                   : c.block == 128 ? (c.half_levels ? F_H128_HALF : F_H128)
                                    : (c.half_levels ? F_H32_HALF : F_H32);
-  const int tiles = (a.N + 15) / 16;
-  // the wide stage unless it costs a token slice or there is too little work
-  // for every warp of the machine to fill one
-  const int most4 = min(c.T, most_tokens(Stage<4>::RING, a.nb)), most8 = min(c.T, most_tokens(Stage<8>::RING, a.nb));
-  const bool wide = most8 > 0 && (c.T + most8 - 1) / most8 == (c.T + most4 - 1) / most4 &&
-                    size_t(tiles) * ((a.nb + 7) / 8) >= size_t(num_sms) * kWarps;
-  const int CB = wide ? 8 : 4, most = wide ? most8 : most4;
-  a.chunks = (a.nb + CB - 1) / CB;
-  a.ny = (c.T + most - 1) / most;
-  a.tt = (c.T + a.ny - 1) / a.ny;
-  a.ny = (c.T + a.tt - 1) / a.tt;
-  // Warps per row tile: the split that ends first.  In cycles, roughly, and
-  // per narrow stage: an SM that is full delivers one every 60; a warp alone
-  // takes 250; joining and storing a tile takes a warp 200, and the SM 20 for
-  // each warp that joins.
-  const int sms = max(1, num_sms / a.ny), per_sm = (tiles + sms - 1) / sms;
-  int best = 0;
-  for (int kg = 1; kg <= min(kWarps, a.chunks); ++kg) {
-    const int gr = min(kWarps / kg, per_sm), w = CB / 4;
-    const int rounds = (per_sm + gr - 1) / gr, stages = (a.chunks + kg - 1) / kg;
-    const int cost = max(per_sm * (a.chunks * w * 60 + kg * 20), rounds * (stages * w * 250 + 200));
-    if (best == 0 || cost < best) {
-      best = cost;
-      a.KG = kg;
-      a.groups = gr;
-    }
+  // the plans of the last shapes (a decode step repeats the same few)
+  struct Entry { int N, nb, T, sms; Plan p; };
+  static thread_local Entry memo[64] = {};
+  Entry& en = memo[(unsigned(a.N) * 31u + unsigned(a.nb) * 7u + unsigned(a.T)) & 63u];
+  if (en.N != a.N || en.nb != a.nb || en.T != a.T || en.sms != num_sms)
+    en = Entry{a.N, a.nb, a.T, num_sms, plan_linear(a.N, a.nb, a.T, num_sms)};
+  const Plan& p = en.p;
+  if (p.cost < 0) return cudaErrorInvalidConfiguration;
+  a.chunks = p.chunks; a.C = p.C; a.cpr = p.cpr; a.KG = p.KG; a.groups = p.groups; a.ny = p.ny; a.tt = p.tt;
+  const int grid = p.C * p.ny * p.ctas;
+  switch (groups_of_8(p.tt) * 16 + p.CB) {
+    case 1 * 16 + 8: return launch_fmt<1, 8>(fmt, a, grid, p.smem, s);
+    case 2 * 16 + 8: return launch_fmt<2, 8>(fmt, a, grid, p.smem, s);
+    case 4 * 16 + 8: return launch_fmt<4, 8>(fmt, a, grid, p.smem, s);
+    case 8 * 16 + 8: return launch_fmt<8, 8>(fmt, a, grid, p.smem, s);
+    case 1 * 16 + 4: return launch_fmt<1, 4>(fmt, a, grid, p.smem, s);
+    case 2 * 16 + 4: return launch_fmt<2, 4>(fmt, a, grid, p.smem, s);
+    case 4 * 16 + 4: return launch_fmt<4, 4>(fmt, a, grid, p.smem, s);
+    default: return launch_fmt<8, 4>(fmt, a, grid, p.smem, s);
   }
-  const int gx = min((tiles + a.groups - 1) / a.groups, sms);
-  const int nt = groups_of_8(a.tt);
-  const size_t smem = linear_smem(wide ? Stage<8>::RING : Stage<4>::RING, a.nb, a.tt, nt);
-  return wide ? launch_stage<8>(fmt, a, nt, gx * a.ny, smem, s) : launch_stage<4>(fmt, a, nt, gx * a.ny, smem, s);
 }
 
 }  // namespace moe
