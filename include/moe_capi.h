@@ -266,6 +266,13 @@ int moe_linear_gated_forward(const moe_config* cfg, const uint8_t* codes, const 
                              const float* row_scales, int32_t inter, int32_t cols, const void* x, int32_t x_type,
                              int32_t T, void* h, int32_t h_type, void* stream);
 
+/* The device check of the two calls above on the current device, as
+ * moe_device_status reads a workspace's (synchronises the device): *code_out =
+ * 0 when no kernel since the last reading reported a failed check, else the
+ * first one's moe_status code, and the return value is MOE_ERR_DEVICE_CHECK.
+ * They have no workspace: the word is a variable of the library. */
+int moe_linear_device_status(int32_t* code_out);
+
 /* The dense gated feed-forward block on 16-bit weights (type MOE_BF16 or
  * MOE_FP16 for every array; what is tuned before it is packed):
  *   g = x Wg^T, u = x Wu^T, h = silu(g) * u, y = h Wd^T

@@ -24,6 +24,7 @@ __all__ = [
     "moe_profile_end", "moe_layer_forward_noalloc", "moe_noalloc_device_status", "NOALLOC_SCRATCH_BYTES",
     "moe_layer_forward_ep", "ep_all_reduce",
     "MOE_BF16", "MOE_FP16", "MOE_FP32", "linear_config_of", "moe_linear_forward", "moe_linear_gated_forward",
+    "moe_linear_device_status",
     "moe_ffn_workspace_bytes", "moe_ffn_forward", "moe_ffn_backward",
 ]
 
@@ -34,7 +35,7 @@ EXPORTS = ("moe_workspace_bytes", "moe_route", "moe_layer_forward", "moe_stack_f
            "moe_layer_forward_noalloc", "moe_last_cuda_error", "moe_debug_fused_timing",
            "moe_debug_prefill_timing", "moe_layer_forward_ep", "moe_debug_decode_path", "moe_debug_wait_probe",
            "moe_noalloc_device_status", "moe_dequant_rows_scaled", "moe_linear_forward",
-           "moe_linear_gated_forward", "moe_ffn_workspace_bytes", "moe_ffn_forward", "moe_ffn_backward")
+           "moe_linear_gated_forward", "moe_linear_device_status", "moe_ffn_workspace_bytes", "moe_ffn_forward", "moe_ffn_backward")
 
 MOE_OK = 0
 MOE_BF16, MOE_FP16, MOE_FP32 = 0, 1, 2      # moe_type
@@ -127,6 +128,8 @@ def load_library(path: str = LIB_PATH):
     lib.moe_linear_forward.restype = ctypes.c_int
     lib.moe_linear_gated_forward.argtypes = [cfgp, P, P, P, I32, I32, P, I32, I32, P, I32, P]
     lib.moe_linear_gated_forward.restype = ctypes.c_int
+    lib.moe_linear_device_status.argtypes = [ctypes.POINTER(ctypes.c_int32)]
+    lib.moe_linear_device_status.restype = ctypes.c_int
     lib.moe_ffn_workspace_bytes.argtypes = [I32, I32, I32, I32]
     lib.moe_ffn_workspace_bytes.restype = SZ
     lib.moe_ffn_forward.argtypes = [I32, I32, I32, P, P, P, I32, P, P, SZ, P]
@@ -397,6 +400,16 @@ def moe_linear_gated_forward(cfg: MoeConfig, codes, scales, x, h, *, row_scales=
     row 2i = gate row i, row 2i + 1 = up row i."""
     return _linear("moe_linear_gated_forward", load_library().moe_linear_gated_forward, cfg, codes, scales, row_scales,
                    None, x, h, 2, stream, check)
+
+
+def moe_linear_device_status() -> int:
+    """The device check word of the packed products on the current device since
+    the last reading (synchronises the device); 0 when none failed."""
+    code = ctypes.c_int32(0)
+    st = load_library().moe_linear_device_status(ctypes.byref(code))
+    if st not in (MOE_OK, -5):
+        _check(st, "moe_linear_device_status")
+    return int(code.value)
 
 
 def moe_ffn_workspace_bytes(hidden: int, inter: int, max_tokens: int, backward: bool = False) -> int:

@@ -28,6 +28,19 @@ struct LinearCall {
 };
 
 cudaError_t launch_linear(const LinearCall& c, int num_sms, cudaStream_t s);
+// Clusters of C CTAs with a full SM each that run at once on this device.
+int clusters_at_once(int C, int num_sms);
+
+// linear_tc.cu: the tensor-core form for larger batches.
+struct TcPlan {
+  int C, cpr, ny, tt, np, nraw, ctas;
+  size_t smem;
+  double cost;           // rough cycles; negative: the shape does not fit
+};
+TcPlan plan_linear_tc(int N, int K, int T, int num_sms);
+cudaError_t launch_linear_tc(const LinearCall& c, const TcPlan& p, cudaStream_t s);
+// The first failed device check of the packed products (code, detail), cleared.
+cudaError_t linear_status(int* out);
 
 struct FfnCall {
   int H, I, T, type;
@@ -78,6 +91,48 @@ __device__ __forceinline__ void store_as(void* p, int type, size_t at, float v) 
   if (type == MOE_FP32) static_cast<float*>(p)[at] = v;
   else if (type == MOE_BF16) static_cast<__nv_bfloat16*>(p)[at] = __float2bfloat16_rn(v);
   else static_cast<__half*>(p)[at] = __float2half_rn(v);
+}
+
+// Eight codes as exact fp16 pairs (e_j, e_{j+4}), j = 0..3.  Integer levels:
+// c - 8; half-integer levels: 2 c - 15, twice the level (halved at the end).
+// A 16-bit lane 0x6400 | m is 1024 + m.
+template <bool HALF>
+__device__ __forceinline__ void code_levels(uint32_t w, uint32_t (&q)[4]) {
+  if (!HALF) {
+    __half2 h[4];
+    decode_q4x8(w, h);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) q[j] = h2_as_u32(h[j]);
+  } else {
+    const uint32_t MAGIC = 0x64006400u;
+    const __half2 sub = u32_as_h2(0x640F640Fu);                                    // 1039 = 1024 + 15
+    const __half2 mul = u32_as_h2(0x30003000u), add = u32_as_h2(0xD878D878u);      // 1/8, -143 = -(128 + 15)
+    q[0] = h2_as_u32(__hsub2(u32_as_h2(lop_and_or(w << 1, 0x001E001Eu, MAGIC)), sub));
+    q[1] = h2_as_u32(__hfma2(u32_as_h2(lop_and_or(w, 0x00F000F0u, MAGIC)), mul, add));
+    q[2] = h2_as_u32(__hsub2(u32_as_h2(lop_and_or(w >> 7, 0x001E001Eu, MAGIC)), sub));
+    q[3] = h2_as_u32(__hfma2(u32_as_h2(lop_and_or(w >> 8, 0x00F000F0u, MAGIC)), mul, add));
+  }
+}
+
+// Eight activations as fp16 pairs (j, j + 4), the order of code_levels.
+__device__ __forceinline__ uint4 pack_activations(const uint4& v, bool bf, float mul) {
+  const uint32_t q[4] = {v.x, v.y, v.z, v.w};
+  float f[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (bf) {
+      f[2 * i] = __uint_as_float(q[i] << 16);
+      f[2 * i + 1] = __uint_as_float(q[i] & 0xffff0000u);
+    } else {
+      const float2 h = __half22float2(u32_as_h2(q[i]));
+      f[2 * i] = h.x;
+      f[2 * i + 1] = h.y;
+    }
+  }
+  uint32_t o[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) o[j] = h2_as_u32(__floats2half2_rn(f[j] * mul, f[j + 4] * mul));
+  return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
 }  // namespace moe

@@ -63,6 +63,7 @@ struct GemmArgs {
   int n, ntiles;
   int bf16;
   int reset;             // 1: the call's first launch clears the status words
+  int split;             // CTAs (pairs) of a cluster that share one tile's reduction
   int* status;
 };
 struct GemmMaps {
@@ -79,12 +80,14 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// Cluster address of the pair's first SM's copy of a shared-memory location.
-__device__ __forceinline__ uint32_t in_leader(const void* p) {
+// Cluster address of CTA `rank`'s copy of a shared-memory location.
+__device__ __forceinline__ uint32_t on_rank(const void* p, int rank) {
   uint32_t a;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(a) : "r"(smem_u32(p)));
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
   return a;
 }
+// Of this CTA's pair's first SM (a pair: ranks 2 i and 2 i + 1).
+__device__ __forceinline__ uint32_t in_leader(const void* p) { return on_rank(p, int(cluster_rank() & ~1u)); }
 template <int CG>
 __device__ __forceinline__ void arrive_leader(uint64_t* bar) {
   if (CG == 1) mbar_arrive(bar);
@@ -114,7 +117,7 @@ __device__ __forceinline__ void commit(uint64_t* bar) {
   else
     asm volatile(
         "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
-        ::"r"(smem_u32(bar)), "h"(uint16_t(3))
+        ::"r"(smem_u32(bar)), "h"(uint16_t(3u << (cluster_rank() & ~1u)))
         : "memory");
 }
 template <int CG>
@@ -200,8 +203,8 @@ __device__ __forceinline__ void load_operand(uint32_t dst, const CUtensorMap* ma
 template <int CG, bool AMN, bool BMN, int BROWS, int STAGE, int STAGES>
 __device__ __forceinline__ bool load_steps(uint32_t ring, uint64_t* full, uint64_t* empty, uint32_t full_leader, int rank,
                                            Cursor<STAGES>& c, const CUtensorMap* ma, const CUtensorMap* mb, int row_a,
-                                           int row_b, int steps, const volatile int* abort_flag) {
-  for (int kb = 0; kb < steps; ++kb) {
+                                           int row_b, int kb0, int steps, const volatile int* abort_flag) {
+  for (int kb = kb0; kb < kb0 + steps; ++kb) {
     if (!mbar_wait(&empty[c.s], c.parity ^ 1u, abort_flag)) return false;
     if (rank == 0) mbar_arrive_expect_tx(&full[c.s], CG * (kAStage + BROWS * 128));
     const uint32_t st = ring + uint32_t(c.s) * STAGE, bar = full_leader + uint32_t(c.s) * 8;
@@ -244,6 +247,34 @@ __device__ __forceinline__ bool settled(uint64_t* bars, Cursor<STAGES> c) {
   return ok;
 }
 
+// Part `rank` of `split` of a reduction of `steps` stages.
+struct Part {
+  int first, steps;
+};
+__device__ __forceinline__ Part part_of(int steps, int split, int rank) {
+  const int per = (steps + split - 1) / split, first = min(rank * per, steps);
+  return {first, min(per, steps - first)};
+}
+// Partial sums of a tile for the cluster's other CTAs: [columns / 4][128 rows]
+// float4, so that a warp's rows are next to each other.
+__device__ __forceinline__ float4* partial(unsigned char* base, int col, int row) {
+  return reinterpret_cast<float4*>(base) + (col >> 2) * 128 + row;
+}
+// Four columns of a row, summed over the parts of the reduction in their order
+// (this CTA's counterparts: ranks place, place + stride, ...).
+__device__ __forceinline__ float4 sum_parts(const float4* p, int split, int place, int stride) {
+  float4 v[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (k < split)
+      asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                   : "=f"(v[k].x), "=f"(v[k].y), "=f"(v[k].z), "=f"(v[k].w) : "r"(on_rank(p, place + k * stride)));
+  }
+  return make_float4((v[0].x + v[1].x) + (v[2].x + v[3].x), (v[0].y + v[1].y) + (v[2].y + v[3].y),
+                     (v[0].z + v[1].z) + (v[2].z + v[3].z), (v[0].w + v[1].w) + (v[2].w + v[3].w));
+}
+
 __device__ __forceinline__ uint32_t pack2(float a, float b, int bf16) {
   if (bf16) {
     const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
@@ -268,6 +299,10 @@ __device__ __forceinline__ void store16(uint16_t* row, int n, int cols, const fl
     if (n < cols) *reinterpret_cast<uint4*>(row + n) = make_uint4(w[0], w[1], w[2], w[3]);
     if (n + 8 < cols) *reinterpret_cast<uint4*>(row + n + 8) = make_uint4(w[4], w[5], w[6], w[7]);
   }
+}
+// Four values (n and the row's column count multiples of 4).
+__device__ __forceinline__ void store4(uint16_t* row, int n, int cols, float a, float b, float c, float d, int bf16) {
+  if (n < cols) *reinterpret_cast<uint2*>(row + n) = make_uint2(pack2(a, b, bf16), pack2(c, d, bf16));
 }
 // All rows of [][ld] start on 32 bytes.
 __device__ __forceinline__ bool on_32(const void* p, int ld) {
@@ -308,7 +343,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ffn_gemm_kernel(const __grid_
   constexpr uint32_t kCols = 2 * BN < 32 ? 32 : 2 * BN;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rank = CG == 1 ? 0 : int(cluster_rank());
+  const int rank = CG == 1 ? 0 : int(cluster_rank() & 1);
+  // with split > 1 the cluster's CTAs or pairs share one tile's reduction
+  const int split = a.split, srank = split > 1 ? int(cluster_rank()) / CG : 0;
   if (threadIdx.x == 0) {
     for (int i = 0; i < T::STAGES; ++i) { mbar_init(&full[i], 1); mbar_init(&empty[i], 1); }
     for (int i = 0; i < 2; ++i) { mbar_init(&acc_full[i], 1); mbar_init(&acc_empty[i], CG * kEpiWarps); }
@@ -326,7 +363,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ffn_gemm_kernel(const __grid_
   pdl_launch_dependents();
   if (a.reset && blockIdx.x == 0 && threadIdx.x == 0) { a.status[0] = 0; a.status[1] = 0; }
 
-  const int unit = int(blockIdx.x) / CG, units = int(gridDim.x) / CG;
+  const int unit = int(blockIdx.x) / (CG * split), units = int(gridDim.x) / (CG * split);
   auto find = [&](int t, int* m, int* n) -> int {
     int i = 0;
     while (i + 1 < a.n && t >= a.p[i + 1].tile0) ++i;
@@ -344,9 +381,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ffn_gemm_kernel(const __grid_
       const int i = find(t, &m, &n);
       const Problem& p = a.p[i];
       const int row_a = m * T::BM + rank * 128, row_b = n * BN + rank * T::BROWS;
+      const Part kp = part_of(p.kblocks, split, srank);
       auto run = [&](auto amn, auto bmn) {
         return load_steps<CG, amn.value, bmn.value, T::BROWS, T::STAGE, T::STAGES>(
-            ring, full, empty, leader, rank, c, &maps.a[i], &maps.b[i], row_a, row_b, p.kblocks, abort_flag);
+            ring, full, empty, leader, rank, c, &maps.a[i], &maps.b[i], row_a, row_b, kp.first, kp.steps, abort_flag);
       };
       ok = p.a_mn ? run(Yes(), Yes()) : p.b_mn ? run(No(), Yes()) : run(No(), No());
     }
@@ -366,9 +404,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ffn_gemm_kernel(const __grid_
       if (!ok) break;
       tc_fence_after();
       const uint32_t idesc = instr_desc(a.bf16, p.a_mn, p.b_mn, T::BM, BN);
+      const Part kp = part_of(p.kblocks, split, srank);
       auto run = [&](auto amn, auto bmn) {
         return mma_steps<CG, amn.value, bmn.value, T::STAGE, T::STAGES>(ring, full, empty, c, tmem + uint32_t(buf * BN),
-                                                                       idesc, p.kblocks, &acc_full[buf], abort_flag);
+                                                                       idesc, kp.steps, &acc_full[buf], abort_flag);
       };
       ok = p.a_mn ? run(Yes(), Yes()) : p.b_mn ? run(No(), Yes()) : run(No(), No());
     }
@@ -389,6 +428,23 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ffn_gemm_kernel(const __grid_
       }
       tc_fence_after();
       const int row = m * T::BM + rank * 128 + q * 32 + lane;
+      if (split > 1) {
+        // this CTA's partial sums for the others, over its ring: all copies
+        // have been used
+#pragma unroll
+        for (int c = 0; c < HC; c += 16) {
+          uint32_t v[16];
+          tmem_ld16(tmem + (uint32_t(q * 32) << 16) + uint32_t(buf * BN + half * HC + c), v);
+          if (row < p.M) {
+#pragma unroll
+            for (int j = 0; j < 16; j += 4)
+              *partial(base, half * HC + c + j, q * 32 + lane) =
+                  make_float4(__uint_as_float(v[j]), __uint_as_float(v[j + 1]), __uint_as_float(v[j + 2]),
+                              __uint_as_float(v[j + 3]));
+          }
+        }
+        break;                         // one tile; joined below
+      }
       const uint32_t tq = tmem + (uint32_t(q * 32) << 16) + uint32_t(buf * BN + half * HC);
       uint16_t* out = static_cast<uint16_t*>(p.out) + size_t(row) * p.ld;
       const bool wide = on_32(p.out, p.ld);
@@ -424,8 +480,35 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ffn_gemm_kernel(const __grid_
   }
 
   __syncwarp();
+  if (split > 1) {
+    // Every CTA of the cluster finishes its share of the tile's columns.
+    cluster_sync();
+    if (warp < kEpiWarps && !*abort_flag) {
+      int m, n;
+      const Problem& p = a.p[find(unit, &m, &n)];
+      const int q = warp & 3, half = warp >> 2, row = m * T::BM + rank * 128 + q * 32 + lane;
+      const int cols = BN / split / 2, c0 = srank * (BN / split) + half * cols;       // 8, 16 or 64
+      if (row < p.M) {
+        uint16_t* out = static_cast<uint16_t*>(p.out) + size_t(row) * p.ld;
+#pragma unroll 2
+        for (int c = c0; c < c0 + cols; c += 8) {
+          const float4 v = sum_parts(partial(base, c, q * 32 + lane), split, rank, CG);
+          const float4 w = sum_parts(partial(base, c + 4, q * 32 + lane), split, rank, CG);
+          const int col = n * BN + c;
+          if (EPI == EPI_STORE) {
+            store4(out, col, p.ld, v.x, v.y, v.z, v.w, a.bf16);
+            store4(out, col + 4, p.ld, w.x, w.y, w.z, w.w, a.bf16);
+          } else {
+            store4(out, col >> 1, p.ld, v.x * sigmoid(v.x) * v.y, v.z * sigmoid(v.z) * v.w, w.x * sigmoid(w.x) * w.y,
+                   w.z * sigmoid(w.z) * w.w, a.bf16);
+          }
+        }
+      }
+    }
+    __syncwarp();
+  }
   tc_fence_before();
-  if (CG == 1) __syncthreads();
+  if (CG == 1 && split == 1) __syncthreads();
   else cluster_sync();
   if (warp == kEpiWarps + 1) {
     tc_fence_after();
@@ -438,6 +521,7 @@ struct GradArgs {
   int T, H, I;
   int tiles_m, tiles_n, kblocks;      // kblocks of one phase (the reduction over H)
   int bf16, reset;
+  int split;                          // narrow tile: CTAs of a cluster that share the reductions
   uint16_t* h;                        // [T][I], or null
   uint16_t* dgu;                      // [T][2I]
   int* status;
@@ -475,6 +559,8 @@ __global__ void __launch_bounds__(kGradThreads, 1) ffn_grad_kernel(const __grid_
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = CG == 1 ? 0 : int(cluster_rank());
+  const int split = CG == 1 ? a.split : 1, srank = split > 1 ? int(cluster_rank()) : 0;
+  const Part kp = part_of(a.kblocks, split, srank);
   if (threadIdx.x == 0) {
     for (int i = 0; i < T::STAGES; ++i) { mbar_init(&full[i], 1); mbar_init(&empty[i], 1); }
     mbar_init(gu_full, 1);
@@ -494,7 +580,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) ffn_grad_kernel(const __grid_
   pdl_launch_dependents();
   if (a.reset && blockIdx.x == 0 && threadIdx.x == 0) { a.status[0] = 0; a.status[1] = 0; }
 
-  const int unit = int(blockIdx.x) / CG, units = int(gridDim.x) / CG;
+  const int unit = int(blockIdx.x) / (CG * split), units = int(gridDim.x) / (CG * split);
   const int ntiles = a.tiles_m * a.tiles_n;
   Problem shape{};
   shape.tiles_m = a.tiles_m;
@@ -509,10 +595,11 @@ __global__ void __launch_bounds__(kGradThreads, 1) ffn_grad_kernel(const __grid_
       tile_of(shape, t, &m, &n);
       const int row_a = m * T::BM + rank * 128;
       ok = load_steps<CG, false, false, T::BROWS, T::STAGE, T::STAGES>(ring, full, empty, leader, rank, c, &tm_x, &tm_wgu,
-                                                                      row_a, n * 2 * NI + rank * T::BROWS, a.kblocks,
+                                                                      row_a, n * 2 * NI + rank * T::BROWS, kp.first, kp.steps,
                                                                       abort_flag) &&
            load_steps<CG, false, true, DROWS, T::STAGE, T::STAGES>(ring, full, empty, leader, rank, c, &tm_dy, &tm_wd,
-                                                                  row_a, n * NI + rank * DROWS, a.kblocks, abort_flag);
+                                                                  row_a, n * NI + rank * DROWS, kp.first, kp.steps,
+                                                                  abort_flag);
     }
     if (!ok) { *abort_flag = 1; report_error(a.status, MOE_ERR_TIMEOUT, 60); }
     if (ok ? !settled(empty, c) : rank == 0 && !settled(full, c)) report_error(a.status, MOE_ERR_TIMEOUT, 61);
@@ -527,13 +614,13 @@ __global__ void __launch_bounds__(kGradThreads, 1) ffn_grad_kernel(const __grid_
       ok = __all_sync(0xffffffffu, mbar_wait(gu_empty, (tc & 1) ^ 1, abort_flag));
       if (!ok) break;
       tc_fence_after();
-      ok = mma_steps<CG, false, false, T::STAGE, T::STAGES>(ring, full, empty, c, tmem, id_gu, a.kblocks, gu_full, abort_flag);
+      ok = mma_steps<CG, false, false, T::STAGE, T::STAGES>(ring, full, empty, c, tmem, id_gu, kp.steps, gu_full, abort_flag);
       if (!ok) break;
       ok = __all_sync(0xffffffffu, mbar_wait(&dh_empty[buf], ((tc >> 1) & 1) ^ 1, abort_flag));
       if (!ok) break;
       tc_fence_after();
       ok = mma_steps<CG, false, true, T::STAGE, T::STAGES>(ring, full, empty, c, tmem + uint32_t(2 * NI + buf * NI), id_dh,
-                                                          a.kblocks, &dh_full[buf], abort_flag);
+                                                          kp.steps, &dh_full[buf], abort_flag);
     }
     if (!ok && lane == 0) { *abort_flag = 1; report_error(a.status, MOE_ERR_TIMEOUT, 62); }
   } else if (warp < kGradEpi) {
@@ -554,6 +641,29 @@ __global__ void __launch_bounds__(kGradThreads, 1) ffn_grad_kernel(const __grid_
         break;
       }
       tc_fence_after();
+      if (split > 1) {
+        // partial sums of g, u (columns 0 to 2 NI) and dh for the others, over
+        // this CTA's ring once all of it has been used
+        ok = mbar_wait(&dh_full[buf], (tc >> 1) & 1, abort_flag);
+        if (!__all_sync(0xffffffffu, ok)) {
+          if (!*abort_flag) { *abort_flag = 1; report_error(a.status, MOE_ERR_TIMEOUT, 67); }
+          break;
+        }
+        tc_fence_after();
+#pragma unroll
+        for (int c = 0; c < 3 * PI; c += 16) {
+          const int col = c < 2 * PI ? 2 * part * PI + c : 2 * NI + part * PI + c - 2 * PI;
+          uint32_t v[16];
+          tmem_ld16(tq + uint32_t(col), v);
+          if (row < a.T) {
+#pragma unroll
+            for (int j = 0; j < 16; j += 4)
+              *partial(base, col + j, q * 32 + lane) = make_float4(__uint_as_float(v[j]), __uint_as_float(v[j + 1]),
+                                                                   __uint_as_float(v[j + 2]), __uint_as_float(v[j + 3]));
+          }
+        }
+        break;
+      }
       float fg[PI], fu[PI];
 #pragma unroll
       for (int c = 0; c < PI; c += 16) {
@@ -607,8 +717,41 @@ __global__ void __launch_bounds__(kGradThreads, 1) ffn_grad_kernel(const __grid_
   }
 
   __syncwarp();
+  if (split > 1) {
+    // Every CTA of the cluster finishes its share of the hidden elements: NI /
+    // split of them, a quarter for each warp of a row quarter.
+    cluster_sync();
+    if (warp < kGradEpi && !*abort_flag) {
+      int m, n;
+      tile_of(shape, unit, &m, &n);
+      const int q = warp & 3, part = warp >> 2, row = m * T::BM + q * 32 + lane;
+      const int per = NI / split / 4, e0 = srank * (NI / split) + part * per;          // 4 or 8
+      if (row < a.T) {
+        for (int e = e0; e < e0 + per; e += 4) {
+          const float4 p0 = sum_parts(partial(base, 2 * e, q * 32 + lane), split, 0, 1);
+          const float4 p1 = sum_parts(partial(base, 2 * e + 4, q * 32 + lane), split, 0, 1);
+          const float4 dh4 = sum_parts(partial(base, 2 * NI + e, q * 32 + lane), split, 0, 1);
+          const float gu[8] = {p0.x, p0.y, p0.z, p0.w, p1.x, p1.y, p1.z, p1.w}, dh[4] = {dh4.x, dh4.y, dh4.z, dh4.w};
+          float h[4], d[8];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float g = gu[2 * j], u = gu[2 * j + 1], s = sigmoid(g), act = g * s;
+            h[j] = act * u;
+            d[2 * j] = dh[j] * (u * fmaf(act, 1.f - s, s));
+            d[2 * j + 1] = dh[j] * act;
+          }
+          const int i = n * NI + e;
+          if (a.h) store4(a.h + size_t(row) * a.I, i, a.I, h[0], h[1], h[2], h[3], a.bf16);
+          uint16_t* out = a.dgu + size_t(row) * 2 * a.I;
+          store4(out, 2 * i, 2 * a.I, d[0], d[1], d[2], d[3], a.bf16);
+          store4(out, 2 * i + 4, 2 * a.I, d[4], d[5], d[6], d[7], a.bf16);
+        }
+      }
+    }
+    __syncwarp();
+  }
   tc_fence_before();
-  if (CG == 1) __syncthreads();
+  if (CG == 1 && split == 1) __syncthreads();
   else cluster_sync();
   if (warp == kGradEpi + 1) {
     tc_fence_after();
@@ -633,22 +776,36 @@ struct Operands {
 
 int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
-// The wide tile (256 x 256 on two SMs) or the narrow one (128 x 64 on one):
-// the one whose busiest SM finishes first.  A 64-deep step takes about 512
-// cycles on the wide tile (its products) and 260 on the narrow one (its
+// CTAs (or pairs, cg = 2) that share one tile's reduction: as many of `most` (4
+// or 2) as leave every tile its own cluster on the machine and each part three
+// stages.
+int split_of(int tiles, int kblocks, int cg, int most, int num_sms) {
+  for (int s = most; s > 1; s /= 2)
+    if (tiles * s * cg <= num_sms / 8 * 8 && kblocks >= 3 * s && (s - 1) * ceil_div(kblocks, s) < kblocks) return s;
+  return 1;
+}
+// Cycles of one product on tiles of `step` cycles per 64-deep step; joining a
+// split tile costs about 4000.
+double tile_time(int tiles, int kblocks, int cg, int most, double step, int num_sms) {
+  const int s = split_of(tiles, kblocks, cg, most, num_sms);
+  return ceil_div(tiles * s, num_sms / cg) * double(ceil_div(kblocks, s)) * step + (s > 1 ? 4000 : 0);
+}
+
+// The wide tile (256 x 256 on two SMs) or the narrow one (128 x 64 on one): the
+// one whose busiest SM finishes first; several products fill each other's last
+// round.  A 64-deep step takes 512 cycles on the wide tile (its products) and
+// about 330 on the narrow one (four instructions at their least time and the
 // operands' way through L2).
 bool wide_tiles(const Problem* p, int n, int num_sms) {
-  double wide = 0, narrow = 0, wmax = 0, nmax = 0;
+  double wide = 0, narrow = 0;
   for (int i = 0; i < n; ++i) {
-    const double w = double(ceil_div(p[i].M, 256)) * ceil_div(p[i].N, 256);
-    const double s = double(ceil_div(p[i].M, 128)) * ceil_div(p[i].N, 64);
-    wide += w * p[i].kblocks;
-    narrow += s * p[i].kblocks;
-    if (p[i].kblocks > wmax) wmax = nmax = p[i].kblocks;
+    const int w = ceil_div(p[i].M, 256) * ceil_div(p[i].N, 256), s = ceil_div(p[i].M, 128) * ceil_div(p[i].N, 64);
+    if (n == 1)
+      return tile_time(w, p[i].kblocks, 2, 2, 512, num_sms) <= tile_time(s, p[i].kblocks, 1, 4, 330, num_sms);
+    wide += double(w) * p[i].kblocks;
+    narrow += double(s) * p[i].kblocks;
   }
-  wide = wide / (num_sms / 2);
-  narrow = narrow / num_sms;
-  return (wide > wmax ? wide : wmax) * 512 <= (narrow > nmax ? narrow : nmax) * 260;
+  return wide / (num_sms / 2) * 512 <= narrow / num_sms * 330;
 }
 
 template <int CG, int BN, int EPI>
@@ -667,8 +824,9 @@ cudaError_t launch_gemm(GemmArgs& a, const Operands* op, int num_sms, cudaStream
       return cudaErrorInvalidValue;
   }
   for (int i = a.n; i < 3; ++i) { maps.a[i] = maps.a[0]; maps.b[i] = maps.b[0]; }
-  const int units = min(num_sms / CG, a.ntiles);
-  return launch_cluster(ffn_gemm_kernel<CG, BN, EPI>, CG, units * CG, kGemmThreads, T::SMEM, s, a, maps);
+  a.split = a.n == 1 ? split_of(a.ntiles, a.p[0].kblocks, CG, CG == 1 ? 4 : 2, num_sms) : 1;
+  const int units = a.split > 1 ? a.ntiles : min(num_sms / CG, a.ntiles), cluster = CG * a.split;
+  return launch_cluster(ffn_gemm_kernel<CG, BN, EPI>, cluster, units * cluster, kGemmThreads, T::SMEM, s, a, maps);
 }
 
 template <int EPI>
@@ -687,8 +845,10 @@ cudaError_t launch_grad(GradArgs& a, const FfnCall& c, int num_sms, cudaStream_t
     return cudaErrorInvalidValue;
   a.tiles_m = ceil_div(c.T, T::BM);
   a.tiles_n = ceil_div(c.I, NI);
-  const int units = min(num_sms / CG, a.tiles_m * a.tiles_n);
-  return launch_cluster(ffn_grad_kernel<CG, NI>, CG, units * CG, kGradThreads, T::SMEM, s, a, x, wgu, dy, wd);
+  const int tiles = a.tiles_m * a.tiles_n;
+  a.split = CG == 1 ? split_of(tiles, a.kblocks, 1, 4, num_sms) : 1;
+  const int units = a.split > 1 ? tiles : min(num_sms / CG, tiles), cluster = CG * a.split;
+  return launch_cluster(ffn_grad_kernel<CG, NI>, cluster, units * cluster, kGradThreads, T::SMEM, s, a, x, wgu, dy, wd);
 }
 
 struct FfnLayout {
@@ -747,8 +907,11 @@ cudaError_t launch_ffn_backward(const FfnCall& c, int num_sms, cudaStream_t s) {
   g.h = c.dw_down ? static_cast<uint16_t*>(h) : nullptr;
   g.dgu = static_cast<uint16_t*>(dgu);
   g.status = reinterpret_cast<int*>(ws + l.status);
-  const Problem gp = problem(c.T, 2 * c.I, c.H, 0, 0, nullptr);
-  cudaError_t e = wide_tiles(&gp, 1, num_sms) ? launch_grad<2, 128>(g, c, num_sms, s) : launch_grad<1, 64>(g, c, num_sms, s);
+  // a step of both reductions: 800 cycles on the wide tile, 600 on the narrow
+  // one, whose reductions can be split
+  const double wide = tile_time(ceil_div(c.T, 256) * ceil_div(c.I, 128), g.kblocks, 2, 1, 800, num_sms);
+  const double narrow = tile_time(ceil_div(c.T, 128) * ceil_div(c.I, 64), g.kblocks, 1, 4, 600, num_sms);
+  cudaError_t e = wide <= narrow ? launch_grad<2, 128>(g, c, num_sms, s) : launch_grad<1, 64>(g, c, num_sms, s);
   if (e != cudaSuccess) return e;
 
   GemmArgs a{};

@@ -102,27 +102,6 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
 }
 
-// Eight codes as exact fp16 pairs (e_j, e_{j+4}), j = 0..3.  Integer levels:
-// c - 8; half-integer levels: 2 c - 15, twice the level (halved at the end).
-// A 16-bit lane 0x6400 | m is 1024 + m.
-template <bool HALF>
-__device__ __forceinline__ void levels(uint32_t w, uint32_t (&q)[4]) {
-  if (!HALF) {
-    __half2 h[4];
-    decode_q4x8(w, h);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) q[j] = h2_as_u32(h[j]);
-  } else {
-    const uint32_t MAGIC = 0x64006400u;
-    const __half2 sub = u32_as_h2(0x640F640Fu);                                    // 1039 = 1024 + 15
-    const __half2 mul = u32_as_h2(0x30003000u), add = u32_as_h2(0xD878D878u);      // 1/8, -143 = -(128 + 15)
-    q[0] = h2_as_u32(__hsub2(u32_as_h2(lop_and_or(w << 1, 0x001E001Eu, MAGIC)), sub));
-    q[1] = h2_as_u32(__hfma2(u32_as_h2(lop_and_or(w, 0x00F000F0u, MAGIC)), mul, add));
-    q[2] = h2_as_u32(__hsub2(u32_as_h2(lop_and_or(w >> 7, 0x001E001Eu, MAGIC)), sub));
-    q[3] = h2_as_u32(__hfma2(u32_as_h2(lop_and_or(w >> 8, 0x00F000F0u, MAGIC)), mul, add));
-  }
-}
-
 // Scales of a row's blocks in a stage as floats (one for all with groups of
 // 128 and CB = 4, two with CB = 8).
 template <int FMT, int CB>
@@ -181,27 +160,6 @@ __device__ __forceinline__ float4 ld_cluster(const void* p, int rank) {
   asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a)
                : "memory");
   return v;
-}
-
-// Eight activations as fp16 pairs (j, j + 4), the order of `levels`.
-__device__ __forceinline__ uint4 pack_activations(const uint4& v, bool bf, float mul) {
-  const uint32_t q[4] = {v.x, v.y, v.z, v.w};
-  float f[8];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if (bf) {
-      f[2 * i] = __uint_as_float(q[i] << 16);
-      f[2 * i + 1] = __uint_as_float(q[i] & 0xffff0000u);
-    } else {
-      const float2 h = __half22float2(u32_as_h2(q[i]));
-      f[2 * i] = h.x;
-      f[2 * i + 1] = h.y;
-    }
-  }
-  uint32_t o[4];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) o[j] = h2_as_u32(__floats2half2_rn(f[j] * mul, f[j + 4] * mul));
-  return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
 template <int NT, int FMT, int CB>
@@ -496,8 +454,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const LinearArgs a)
         // fold: the sums so far take the scale of block b
         auto block = [&](int b, bool start, bool fold) {
           uint32_t q0[4], q1[4];
-          levels<F::HALF>(*reinterpret_cast<const uint32_t*>(lsm + (code0 ^ (b << 4))), q0);
-          levels<F::HALF>(*reinterpret_cast<const uint32_t*>(lsm + (code0 ^ (b << 4)) + 8 * S::ROW), q1);
+          code_levels<F::HALF>(*reinterpret_cast<const uint32_t*>(lsm + (code0 ^ (b << 4))), q0);
+          code_levels<F::HALF>(*reinterpret_cast<const uint32_t*>(lsm + (code0 ^ (b << 4)) + 8 * S::ROW), q1);
           const uint32_t lo[4] = {q0[0], q1[0], q0[1], q1[1]}, hi[4] = {q0[2], q1[2], q0[3], q1[3]};
 #pragma unroll
           for (int j = 0; j < NT; ++j) {
@@ -599,45 +557,15 @@ cudaError_t launch_fmt(int fmt, const LinearArgs& a, int grid, size_t smem, cuda
 
 int groups_of_8(int tt) { return tt <= 8 ? 1 : tt <= 16 ? 2 : tt <= 32 ? 4 : 8; }
 
-// Clusters of C CTAs with a full SM each that run at once on this device.
-int clusters_at_once(int C, int num_sms) {
-  static int cached[64][4] = {};
-  if (C == 1) return num_sms;
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return num_sms / 8 * 8 / C;
-  int& n = cached[dev][C == 2 ? 1 : C == 4 ? 2 : 3];
-  if (n == 0) {
-    auto kern = linear_kernel<1, F_H32, 4>;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(num_sms / C * C);
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = 200 * 1024;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = unsigned(C);
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    int got = 0;
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024) != cudaSuccess ||
-        cudaOccupancyMaxActiveClusters(&got, kern, &cfg) != cudaSuccess || got <= 0) {
-      (void)cudaGetLastError();
-      got = max(1, num_sms / 8 * 8 / C);
-    }
-    n = got;
-  }
-  return n;
-}
-
 struct Plan {
   int C, CB, cpr, chunks, KG, groups, tt, ny, ctas;
   size_t smem;
   double cost;
 };
 
-// The launch that ends first by a rough count of cycles (fitted to measured
-// calls): converting a CTA's activations, its share of the blocks at the rate
-// the warps' instructions issue (38 + 9 for each 8 tokens, 2.5 a cycle), or a
+// The launch that ends first by a rough count of cycles, fitted to measured
+// calls (40000 x 2048: 8, 16, 32, 64 tokens 17.6, 33, 64 and 98 cycles a block
+// of 16 x 32): converting a CTA's activations, its share of the blocks, or a
 // warp's own chain of stages where there are few.
 Plan plan_linear(int N, int nb, int T, int num_sms) {
   Plan best{};
@@ -672,10 +600,10 @@ Plan plan_linear(int N, int nb, int T, int num_sms) {
         p.smem = linear_smem(ring, CB, p.cpr, p.tt, groups_of_8(p.tt), p.groups, KG, C);
         const int NT = groups_of_8(p.tt), per = (tiles + p.ctas - 1) / p.ctas, waves = (p.ny * p.ctas + at_once - 1) / at_once;
         const int rounds = (per + p.groups - 1) / p.groups, stages = (p.cpr + KG - 1) / KG;
-        const double block = (38 + 9 * NT) / 2.5, stage = 200 + CB * (20 + 6 * NT);
+        const double block = 6 + 13.5 * NT, stage = 250 + CB * (25 + 15 * NT);
         const double thr = per * (double(p.cpr) * CB * block + 60 + KG * (10 + 4 * NT));
         const double lat = rounds * (stages * stage + 200 + (C > 1 ? 100 : 0));
-        p.cost = waves * (1000 + p.tt * double(p.cpr) * CB * 32 * 0.08 + (C > 1 ? 1500 : 0) + (thr > lat ? thr : lat));
+        p.cost = waves * (5000 + p.tt * double(p.cpr) * CB * 32 * 0.1 + (C > 1 ? 2500 : 0) + (thr > lat ? thr : lat));
         if (best.cost < 0 || p.cost < best.cost) best = p;
       }
     }
@@ -684,6 +612,36 @@ Plan plan_linear(int N, int nb, int T, int num_sms) {
 }
 
 }  // namespace
+
+// Clusters of C CTAs with a full SM each that run at once on this device.
+int clusters_at_once(int C, int num_sms) {
+  static int cached[64][4] = {};
+  if (C == 1) return num_sms;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return num_sms / 8 * 8 / C;
+  int& n = cached[dev][C == 2 ? 1 : C == 4 ? 2 : 3];
+  if (n == 0) {
+    auto kern = linear_kernel<1, F_H32, 4>;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(num_sms / C * C);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = 200 * 1024;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = unsigned(C);
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int got = 0;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&got, kern, &cfg) != cudaSuccess || got <= 0) {
+      (void)cudaGetLastError();
+      got = max(1, num_sms / 8 * 8 / C);
+    }
+    n = got;
+  }
+  return n;
+}
 
 cudaError_t launch_linear(const LinearCall& c, int num_sms, cudaStream_t s) {
   LinearArgs a{};
@@ -696,12 +654,17 @@ cudaError_t launch_linear(const LinearCall& c, int num_sms, cudaStream_t s) {
                   : c.block == 128 ? (c.half_levels ? F_H128_HALF : F_H128)
                                    : (c.half_levels ? F_H32_HALF : F_H32);
   // the plans of the last shapes (a decode step repeats the same few)
-  struct Entry { int N, nb, T, sms; Plan p; };
+  struct Entry { int N, nb, T, sms; Plan p; TcPlan tc; };
   static thread_local Entry memo[64] = {};
   Entry& en = memo[(unsigned(a.N) * 31u + unsigned(a.nb) * 7u + unsigned(a.T)) & 63u];
   if (en.N != a.N || en.nb != a.nb || en.T != a.T || en.sms != num_sms)
-    en = Entry{a.N, a.nb, a.T, num_sms, plan_linear(a.N, a.nb, a.T, num_sms)};
+    en = Entry{a.N, a.nb, a.T, num_sms, plan_linear(a.N, a.nb, a.T, num_sms), plan_linear_tc(a.N, a.K, a.T, num_sms)};
   const Plan& p = en.p;
+  // more than one group of 8 tokens and results of 16 bits: the tensor-core
+  // form where its count is clearly the smaller one (32 tokens: 40000 x 2048 26
+  // against 41 us, 2048 x 2048 12 against 9 us)
+  if (c.y_type != MOE_FP32 && c.T > 8 && en.tc.cost >= 0 && (p.cost < 0 || en.tc.cost < 0.85 * p.cost))
+    return launch_linear_tc(c, en.tc, s);
   if (p.cost < 0) return cudaErrorInvalidConfiguration;
   a.chunks = p.chunks; a.C = p.C; a.cpr = p.cpr; a.KG = p.KG; a.groups = p.groups; a.ny = p.ny; a.tt = p.tt;
   const int grid = p.C * p.ny * p.ctas;

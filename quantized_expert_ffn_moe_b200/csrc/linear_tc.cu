@@ -1,0 +1,656 @@
+// The packed products of linear.cu for larger decode batches with 16-bit
+// results, on the tcgen05 tensor cores: the warp-level instructions of
+// linear.cu cost the issue slots of a dequantisation again for every 8 tokens,
+// here a code is dequantised once for up to 64 of them.
+//
+// Per tile of 128 rows: D[128 x N tokens] (fp32, tensor memory) = W (fp16,
+// dequantised into tensor memory) . X^T (fp16, resident in shared memory).
+// A weight is q * s rounded to fp16 once (at most 2^-11 of its value, less than a
+// quarter of what the result's own rounding to bf16 adds; results in fp32 stay
+// with the exact kernel).  So that neither overflow nor fp16's least step
+// matters, a row's scales are first multiplied by the power of two that brings
+// the largest of them (of this CTA's columns) into [2^10, 2^11); with E4M3
+// scales q * s is exact and the row scale is applied at the end.  Activations
+// as in linear.cu.
+//
+// The CTAs of a cluster split the columns: each converts and keeps its own
+// columns of X alone, and the tile's partial sums are added over distributed
+// shared memory in rank order.  Warp roles: one thread copies the packed codes
+// (tensor copies, 128 rows x 128 columns a stage), one warp issues the
+// products, four read the accumulators out (and look for the next rows'
+// largest scales), sixteen dequantise: four sets of four warps (one per
+// quarter of the tensor memory's lanes) take the stages in turn.  A stage is
+// eight instructions of 128 x N x 16, at least 55 cycles each, so about 37
+// weights a cycle and SM; the HBM rate is 46.  Every wait is bounded.
+#include "dense_internal.cuh"
+#include "tensor_core.cuh"
+
+namespace moe {
+
+// First failed check of the packed products on this device (a moe_status code
+// and its detail): they have no workspace to keep it in.
+__device__ int g_linear_status[2];
+
+namespace {
+
+constexpr int kSets = 4;                          // dequantising sets of four warps
+constexpr int kWarpCopy = 0, kWarpMma = 1, kWarpDq = 6;      // 2 to 5: results
+constexpr int kWarps = kWarpDq + 4 * kSets;
+constexpr int kThreads = kWarps * 32;
+constexpr int kRawBytes = 128 * 64;               // packed codes of a stage
+constexpr int kMaxRaw = 8;                        // ring of packed stages (4 to 8)
+constexpr int kA = 6;                             // dequantised stages in tensor memory
+constexpr uint32_t kACol = 128;                   // after two accumulators of 64 columns
+static_assert(kACol + kA * 64 <= 512, "tensor memory");
+constexpr int kBars = 512;
+constexpr size_t kMaxSmem = 232448;
+
+struct TcArgs {
+  const void* scales;
+  const float* row_scales;
+  const float* bias;
+  const void* x;
+  void* y;
+  int N, K, T;
+  int spr;                 // scales of a row
+  int stages;              // 128-column stages of a row
+  int C, cpr;              // CTAs of a cluster, stages that each takes
+  int ny, tt, np;          // token slices, tokens of a slice, those rounded up to 16
+  int nraw;
+  int x_type, y_type, gated;
+};
+
+enum { F_H32 = 0, F_H128 = 1, F_E32 = 2 };
+
+__device__ __forceinline__ uint32_t on_rank(const void* p, int rank) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+  return a;
+}
+__device__ __forceinline__ void arrive_on(uint64_t* bar, int rank) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(on_rank(bar, rank)) : "memory");
+}
+__device__ __forceinline__ float ld_on(const float* p, int rank) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(on_rank(p, rank)));
+  return v;
+}
+// mbar_wait that also sees what the cluster's CTAs wrote before they arrived.
+__device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity, const volatile int* abort_flag) {
+  const long long t0 = clock64();
+  while (true) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok) : "r"(smem_u32(bar)), "r"(parity) : "memory");
+    if (ok) return true;
+    if (abort_flag && *abort_flag) return false;
+    if (clock64() - t0 > kWaitLimitCycles) return false;
+  }
+}
+// Shared-memory stores of this thread made visible to the asynchronous proxy.
+__device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void commit1(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
+               : "memory");
+}
+// A from tensor memory (lane = row, two fp16 a column), B from shared memory.
+__device__ __forceinline__ void mma_ta(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+      ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void st32(uint32_t taddr, const uint32_t v[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};"
+      ::"r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
+        "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]),
+        "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]),
+        "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
+      : "memory");
+}
+__device__ __forceinline__ void ld16(uint32_t taddr, uint32_t v[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+        "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+      : "r"(taddr));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+
+// The scales of a row's blocks in one stage: raw bytes, loaded ahead.
+template <int FMT>
+struct StageScales {
+  static constexpr int PER = FMT == F_H128 ? 1 : 4;
+  uint16_t s[PER];
+  static constexpr int SB = FMT == F_E32 ? 1 : 2;
+  // row: the row's scales
+  __device__ __forceinline__ void load(const uint8_t* row, int stage, int spr, bool aligned) {
+    const uint8_t* at = row + stage * (PER * SB);
+    if (FMT == F_H128) {
+      s[0] = __ldg(reinterpret_cast<const uint16_t*>(at));
+    } else if (aligned) {
+      if (FMT == F_H32) {
+        const uint2 v = __ldg(reinterpret_cast<const uint2*>(at));
+        s[0] = uint16_t(v.x); s[1] = uint16_t(v.x >> 16); s[2] = uint16_t(v.y); s[3] = uint16_t(v.y >> 16);
+      } else {
+        const uint32_t v = __ldg(reinterpret_cast<const uint32_t*>(at));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[i] = uint16_t((v >> (8 * i)) & 0xff);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        s[i] = 0;
+        if (stage * 4 + i < spr) s[i] = SB == 2 ? __ldg(reinterpret_cast<const uint16_t*>(at) + i) : uint16_t(__ldg(at + i));
+      }
+    }
+  }
+  // of block i as a pair, fp16 scales times the row's power of two
+  __device__ __forceinline__ __half2 pair(int i, __half2 norm) const {
+    if (FMT == F_E32) {
+      uint32_t h;
+      asm("{\n\t.reg .b16 a;\n\tmov.b16 a, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\t}" : "=r"(h) : "h"(s[i]));
+      return __low2half2(u32_as_h2(h));
+    }
+    return __hmul2(__half2half2(__ushort_as_half(s[FMT == F_H128 ? 0 : i])), norm);
+  }
+};
+
+template <int FMT, bool HALF>
+__global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const TcArgs a, const __grid_constant__ CUtensorMap tm) {
+  extern __shared__ __align__(1024) unsigned char csm_raw[];
+  unsigned char* base = csm_raw + ((0u - smem_u32(csm_raw)) & 1023u);
+  unsigned char* sraw = base;                                           // [nraw] stages of codes
+  unsigned char* sx = sraw + a.nraw * kRawBytes;                        // [2 cpr] blocks of 64 columns: [np] rows of 128 bytes
+  float* sout = reinterpret_cast<float*>(sx + size_t(a.cpr) * 2 * a.np * 128);   // C > 1: [2][np][128]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sout + (a.C > 1 ? 2 * a.np * 128 : 0));
+  uint64_t* full_raw = bars;
+  uint64_t* empty_raw = full_raw + kMaxRaw;
+  uint64_t* full_a = empty_raw + kMaxRaw;
+  uint64_t* empty_a = full_a + kA;
+  uint64_t* acc_full = empty_a + kA;
+  uint64_t* acc_empty = acc_full + 2;
+  uint64_t* norm_full = acc_empty + 2;        // the rows' powers of two of a tile are in snorm
+  uint64_t* norm_empty = norm_full + 2;
+  uint64_t* joined = norm_empty + 2;          // C > 1: every CTA's sums of a tile are in its sout
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(joined + 2);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  float* snorm = reinterpret_cast<float*>(reinterpret_cast<unsigned char*>(bars) + kBars);   // [2][128]
+  float* sinv = snorm + 256;                                            // [64]
+  uint32_t* smax = reinterpret_cast<uint32_t*>(sinv + 64);              // [tt][kWarps]
+
+  const int warp = __shfl_sync(0xffffffffu, int(threadIdx.x) >> 5, 0), lane = threadIdx.x & 31;
+  const int rank = int(blockIdx.x % unsigned(a.C)), unit = int(blockIdx.x / unsigned(a.C));
+  const int slice = unit % a.ny, cta = unit / a.ny, ctas = int(gridDim.x / unsigned(a.C * a.ny));
+  const int t0 = slice * a.tt, nt = min(a.tt, a.T - t0);
+  const int c_lo = rank * a.cpr, ns = min(a.cpr, a.stages - c_lo);      // this CTA's stages of a row
+  const int ntiles = (a.N + 127) >> 7;
+  const int my_tiles = (ntiles - cta + ctas - 1) / ctas;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < a.nraw; ++i) { mbar_init(&full_raw[i], 1); mbar_init(&empty_raw[i], 4); }
+    for (int i = 0; i < kA; ++i) { mbar_init(&full_a[i], 4); mbar_init(&empty_a[i], 1); }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&acc_full[i], 1);
+      mbar_init(&acc_empty[i], 4);
+      mbar_init(&norm_full[i], 4);
+      mbar_init(&norm_empty[i], 4 * kSets);
+      mbar_init(&joined[i], 4 * a.C);
+    }
+    *abort_flag = 0;
+    mbar_fence_init();
+  }
+  const int total = my_tiles * ns, ahead = min(a.nraw, total);
+  // the first packed stages do not depend on the previous kernel of the stream
+  if (threadIdx.x == 0) {
+    for (int i = 0, tile = cta, c = 0; i < ahead; ++i) {
+      mbar_arrive_expect_tx(&full_raw[i], kRawBytes);
+      tma_load_2d(sraw + i * kRawBytes, &tm, (c_lo + c) * 64, tile * 128, &full_raw[i]);
+      if (++c == ns) { c = 0; tile += ctas; }
+    }
+  }
+  __syncwarp();
+  if (warp == kWarpMma) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "r"(512u)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  // The result warps look for the power of two of their rows of a tile, the
+  // dequantising ones load their first scales: before the wait for the
+  // activations, the weights do not depend on the previous kernel.
+  const int q = warp & 3, r = q * 32 + lane;     // quarter of the tensor memory's lanes, row of a tile
+  float inv_norm[2] = {1.f, 1.f};
+  // the largest scale (fp16 bits) of this lane's row of tile i
+  auto row_top = [&](int i) -> uint32_t {
+    if (FMT == F_E32 || i >= my_tiles) return 0u;
+    const uint16_t* p = static_cast<const uint16_t*>(a.scales) + size_t(min((cta + i * ctas) * 128 + r, a.N - 1)) * a.spr;
+    const int per = FMT == F_H128 ? 1 : 4, lo = c_lo * per, hi = min(a.spr, (c_lo + ns) * per);
+    uint32_t m = 0;
+    int k = lo;
+    if (a.spr % 8 == 0 && lo % 8 == 0) {
+#pragma unroll 4
+      for (; k + 8 <= hi; k += 8) {
+        const uint4 v = __ldg(reinterpret_cast<const uint4*>(p + k));
+        m = __vmaxu2(m, __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu),
+                                 __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu)));
+      }
+    }
+    m = max(m & 0xffffu, m >> 16);
+    for (; k < hi; ++k) m = max(m, uint32_t(__ldg(p + k)) & 0x7fffu);
+    return m;
+  };
+  // its power of two, into snorm; the inverse is returned
+  auto put_norm = [&](int i, uint32_t m) {
+    float up = 1.f, down = 1.f;
+    if (m > 0 && m < 0x7c00u) {
+      int ex;
+      frexpf(__half2float(__ushort_as_half((unsigned short)m)), &ex);
+      // fp16 holds 2^-14 to 2^15; larger powers are not needed: 2^15 times the least scale is 2^-9
+      const int sh = min(max(11 - ex, -14), 15);
+      up = ldexpf(1.f, sh);
+      down = ldexpf(1.f, -sh);
+    }
+    snorm[(i & 1) * 128 + r] = up;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&norm_full[i & 1]);
+    return down;
+  };
+  const bool results = warp > kWarpMma && warp < kWarpDq;
+  const bool aligned = FMT != F_H128 && a.spr % 4 == 0;
+  const int set = (warp - kWarpDq) >> 2;
+  auto scale_row = [&](int tile) {
+    return static_cast<const uint8_t*>(a.scales) +
+           size_t(min((cta + tile * ctas) * 128 + r, a.N - 1)) * a.spr * StageScales<FMT>::SB;
+  };
+  StageScales<FMT> next;
+  const uint8_t* next_row = nullptr;
+  int dq_tile = 0, dq_c = 0;
+  uint32_t top0 = 0, top1 = 0;
+  if (results) {
+    top0 = row_top(0);
+    top1 = row_top(1);
+  } else if (warp >= kWarpDq && set < total) {
+    dq_tile = set / ns;
+    dq_c = set - dq_tile * ns;
+    next_row = scale_row(dq_tile);
+    next.load(next_row, c_lo + dq_c, a.spr, aligned);
+  }
+  tc_fence_before();
+  if (a.C > 1) cluster_sync();               // the barriers are there before another CTA arrives on them
+  else __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  if (results) {
+    inv_norm[0] = put_norm(0, top0);
+    if (my_tiles > 1) inv_norm[1] = put_norm(1, top1);
+  }
+  pdl_wait();
+  pdl_launch_dependents();
+
+  // ------------------------------------------------------ activations
+  // Rows of this CTA's columns as fp16 (scaled and in the pair order of the
+  // codes, as in linear.cu), in the K-major 128-byte swizzle; columns past the
+  // matrix and tokens past the slice are 0.
+  {
+    const int col0 = c_lo * 128, W = a.cpr * 16;          // 16-byte words of a row of sx
+    const int K8 = min(a.K - col0, ns * 128) >> 3;        // those inside the matrix
+    const bool bf = a.x_type == MOE_BF16;
+    const uint16_t* xb = static_cast<const uint16_t*>(a.x) + size_t(t0) * a.K + col0;
+    const int sl = nt >= kWarps ? 1 : kWarps / nt, units = nt * sl, per = (W + sl - 1) / sl;
+    constexpr int HOLD = 14;
+    // one unit a warp and HOLD words a lane: kept between the two passes
+    const bool held = units <= kWarps && per <= HOLD * 32;
+    uint4 v[HOLD];
+    for (int u = warp; u < units; u += kWarps) {
+      const int n = u / sl, p = u - n * sl, end = min(K8, (p + 1) * per);
+      const uint4* src = reinterpret_cast<const uint4*>(xb + size_t(n) * a.K);
+      uint32_t m = 0;
+      for (int w0 = p * per; w0 < end; w0 += HOLD * 32) {
+#pragma unroll
+        for (int i = 0; i < HOLD; ++i) v[i] = w0 + i * 32 + lane < end ? __ldg(src + w0 + i * 32 + lane) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int i = 0; i < HOLD; ++i)
+          m = __vmaxu2(m, __vmaxu2(__vmaxu2(v[i].x & 0x7fff7fffu, v[i].y & 0x7fff7fffu),
+                                   __vmaxu2(v[i].z & 0x7fff7fffu, v[i].w & 0x7fff7fffu)));
+      }
+      m = __reduce_max_sync(0xffffffffu, max(m & 0xffffu, m >> 16));
+      if (lane == 0) smax[n * kWarps + p] = m;
+    }
+    __syncthreads();
+    for (int u = warp; u < a.np * sl; u += kWarps) {
+      const int n = u / sl, p = u - n * sl, end = min(W, (p + 1) * per);
+      float mul = 0.f;
+      if (n < nt) {
+        uint32_t m = lane < sl ? smax[n * kWarps + lane] : 0u;
+        m = __reduce_max_sync(0xffffffffu, m);
+        const bool finite = m < (bf ? 0x7f80u : 0x7c00u);
+        const float top = bf ? __uint_as_float(m << 16) : __half2float(__ushort_as_half((unsigned short)m));
+        int sh = 0;
+        if (finite && top > 0.f) {
+          int ex;
+          frexpf(top, &ex);
+          sh = min(max(14 - ex, -120), 120);
+        }
+        mul = ldexpf(1.f, sh);
+        if (p == 0 && lane == 0) sinv[n] = finite ? ldexpf(HALF ? 0.5f : 1.f, -sh) : __int_as_float(0x7fc00000);
+      }
+      const uint4* src = reinterpret_cast<const uint4*>(xb + size_t(n) * a.K);
+      for (int w0 = p * per; w0 < end; w0 += HOLD * 32) {
+        if (!held || u >= units) {
+#pragma unroll
+          for (int i = 0; i < HOLD; ++i) {
+            const int w = w0 + i * 32 + lane;
+            v[i] = n < nt && w < min(end, K8) ? __ldg(src + w) : make_uint4(0, 0, 0, 0);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < HOLD; ++i) {
+          const int w = w0 + i * 32 + lane;
+          if (w < end)
+            *reinterpret_cast<uint4*>(sx + size_t(w >> 3) * (a.np * 128) + n * 128 + (((w & 7) ^ (n & 7)) << 4)) =
+                pack_activations(v[i], bf, mul);
+        }
+      }
+    }
+    fence_async_smem();
+    __syncthreads();
+  }
+
+  if (warp == kWarpCopy) {
+    if (lane == 0) {
+      // ------------------------------------------------- packed codes
+      int s = 0, c = 0, tile = cta;
+      uint32_t ph = 0;
+      bool ok = true;
+      for (int i = 0; i < total; ++i) {
+        if (i >= ahead) {
+          if (!mbar_wait(&empty_raw[s], ph ^ 1u, abort_flag)) { ok = false; break; }
+          mbar_arrive_expect_tx(&full_raw[s], kRawBytes);
+          tma_load_2d(sraw + s * kRawBytes, &tm, (c_lo + c) * 64, tile * 128, &full_raw[s]);
+        }
+        if (++s == a.nraw) { s = 0; ph ^= 1u; }
+        if (++c == ns) { c = 0; tile += ctas; }
+      }
+      if (!ok) {
+        *abort_flag = 1;
+        report_error(g_linear_status, MOE_ERR_TIMEOUT, 80);
+      }
+      // no copy is under way when the CTA leaves: every used slot's last phase
+      for (int i = 0; i < a.nraw; ++i) {
+        mbar_wait(&full_raw[s], ph ^ 1u, nullptr);
+        if (++s == a.nraw) { s = 0; ph ^= 1u; }
+      }
+    }
+  } else if (warp == kWarpMma) {
+    // ------------------------------------------------------- products
+    const uint32_t idesc = (1u << 4) | (uint32_t(a.np >> 3) << 17) | (8u << 24);     // fp32 += fp16 x fp16, M = 128
+    const uint64_t b0 = sw128_desc(smem_u32(sx));
+    const uint32_t bstep = uint32_t(a.np * 128) >> 4;                              // a block of 64 columns
+    int s = 0;
+    uint32_t ph = 0;
+    bool ok = true;
+    for (int i = 0; i < my_tiles && ok; ++i) {
+      const int buf = i & 1;
+      ok = __all_sync(0xffffffffu, mbar_wait(&acc_empty[buf], ((i >> 1) & 1) ^ 1, abort_flag));
+      if (!ok) break;
+      tc_fence_after();
+      for (int c = 0; c < ns; ++c) {
+        ok = __all_sync(0xffffffffu, mbar_wait(&full_a[s], ph, abort_flag));
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_one()) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            mma_ta(tmem + uint32_t(buf * 64), tmem + kACol + uint32_t(s * 64 + k * 8),
+                   b0 + uint64_t((2 * c + (k >> 2)) * bstep + ((k & 3) * 32 >> 4)), idesc, (c | k) ? 1u : 0u);
+          commit1(&empty_a[s]);
+          if (c == ns - 1) commit1(&acc_full[buf]);
+        }
+        __syncwarp();
+        if (++s == kA) { s = 0; ph ^= 1u; }
+      }
+    }
+    if (!ok && lane == 0) {
+      *abort_flag = 1;
+      report_error(g_linear_status, MOE_ERR_TIMEOUT, 81);
+    }
+    // the last products are done before the tensor memory goes
+    for (int i = 0; i < kA; ++i) {
+      mbar_wait(&empty_a[s], ph ^ 1u, ok ? nullptr : abort_flag);
+      if (++s == kA) { s = 0; ph ^= 1u; }
+    }
+  } else if (warp >= kWarpDq) {
+    // --------------------------------------------------- dequantising
+    const uint32_t lanes = uint32_t(q * 32) << 16;
+    // this set's stages: total counter i = set, set + kSets, ...
+    int i = set, tl = dq_tile, c = dq_c;
+    // its places in the two rings and their parities, kSets on each time
+    int raw = set, as = set;
+    uint32_t raw_ph = 0, as_ph = 0;
+    static_assert(kSets <= 4 && kSets <= kA, "a set's first stages are in the first round of both rings");
+    int seen = -1;                                   // the tile whose powers of two are in `norm`
+    __half2 norm = __float2half2_rn(1.f);
+    bool ok = true;
+    // every tile's powers of two are taken and released once, also of a tile
+    // that holds no stage of this set
+    auto take_norms = [&](int tile) {
+      if constexpr (FMT != F_E32) {
+        for (; seen < tile && ok; ++seen) {
+          const int u = seen + 1;
+          ok = __all_sync(0xffffffffu, mbar_wait(&norm_full[u & 1], (u >> 1) & 1, abort_flag));
+          if (!ok) break;
+          norm = __float2half2_rn(snorm[(u & 1) * 128 + r]);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&norm_empty[u & 1]);
+        }
+      }
+    };
+    for (; i < total; i += kSets) {
+      const StageScales<FMT> cur = next;
+      const int tile_i = tl;
+      c += kSets;
+      if (c >= ns) {
+        do { c -= ns; ++tl; } while (c >= ns);
+        next_row = scale_row(min(tl, my_tiles - 1));
+      }
+      if (i + kSets < total) next.load(next_row, c_lo + c, a.spr, aligned);
+      take_norms(tile_i);
+      ok = ok && __all_sync(0xffffffffu, mbar_wait(&full_raw[raw], raw_ph, abort_flag) &&
+                                             mbar_wait(&empty_a[as], as_ph ^ 1u, abort_flag));
+      if (!ok) break;
+      tc_fence_after();
+      const unsigned char* row = sraw + raw * kRawBytes + r * 64;
+      const int sw = (r >> 1) & 3;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t o[32];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int blk = 2 * h + e;
+          const uint4 w = *reinterpret_cast<const uint4*>(row + ((blk ^ sw) << 4));
+          const __half2 s2 = cur.pair(blk, norm);
+          const uint32_t wd[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+          for (int z = 0; z < 4; ++z) {
+            uint32_t lv[4];
+            code_levels<HALF>(wd[z], lv);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) o[e * 16 + z * 4 + j] = h2_as_u32(__hmul2(u32_as_h2(lv[j]), s2));
+          }
+        }
+        st32(tmem + lanes + kACol + uint32_t(as * 64 + h * 32), o);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&empty_raw[raw]);
+      asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&full_a[as]);
+      if ((raw += kSets) >= a.nraw) { raw -= a.nraw; raw_ph ^= 1u; }
+      if ((as += kSets) >= kA) { as -= kA; as_ph ^= 1u; }
+    }
+    if (ok) take_norms(my_tiles - 3);                // the last whose place is filled again
+    if (!ok && lane == 0 && !*abort_flag) {
+      *abort_flag = 1;
+      report_error(g_linear_status, MOE_ERR_TIMEOUT, 82);
+    }
+  } else {
+    // ------------------------------------------------------- results
+    bool ok = true;
+    for (int i = 0; i < my_tiles; ++i) {
+      const int buf = i & 1;
+      const uint32_t top = row_top(i + 2);         // its loads end under this tile's products
+      ok = __all_sync(0xffffffffu, mbar_wait(&acc_full[buf], (i >> 1) & 1, abort_flag));
+      if (!ok) break;
+      tc_fence_after();
+      const int row0 = (cta + i * ctas) * 128, row = row0 + r;
+      const float down = buf ? inv_norm[1] : inv_norm[0];
+      const float rs = FMT == F_E32 ? __ldg(a.row_scales + min(row, a.N - 1)) : 1.f;
+      const float bias = a.bias ? __ldg(a.bias + min(row, a.N - 1)) : 0.f;
+      // one token's result of this lane's row (of its pair of rows when gated)
+      auto finish = [&](float v, int n) {
+        v *= rs;
+        if (!a.gated) {
+          if (row < a.N) store_as(a.y, a.y_type, size_t(t0 + n) * a.N + row, v + bias);
+        } else {
+          const float other = __shfl_xor_sync(0xffffffffu, v, 1);
+          if (!(lane & 1) && row < a.N)
+            store_as(a.y, a.y_type, size_t(t0 + n) * (a.N >> 1) + (row >> 1), v / (1.f + expf(-v)) * other);
+        }
+      };
+      float* so = sout + buf * a.np * 128 + r;
+#pragma unroll 1
+      for (int n0 = 0; n0 < nt; n0 += 16) {
+        uint32_t v[16];
+        ld16(tmem + (uint32_t(q * 32) << 16) + uint32_t(buf * 64 + n0), v);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          if (n0 + j >= nt) break;
+          const float f = __uint_as_float(v[j]) * down * sinv[n0 + j];
+          if (a.C == 1) finish(f, n0 + j);
+          else so[(n0 + j) * 128] = f;
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&acc_empty[buf]);
+      if (i + 2 < my_tiles) {            // the powers of two after the next, once every set has taken this tile's
+        if (FMT != F_E32) {
+          ok = __all_sync(0xffffffffu, mbar_wait(&norm_empty[buf], (i >> 1) & 1, abort_flag));
+          if (!ok) break;
+        }
+        const float d = put_norm(i + 2, top);
+        if (buf) inv_norm[1] = d;
+        else inv_norm[0] = d;
+      }
+      if (a.C > 1) {
+        if (lane < a.C) arrive_on(&joined[buf], lane);
+        __syncwarp();
+        ok = __all_sync(0xffffffffu, wait_cluster(&joined[buf], (i >> 1) & 1, abort_flag));
+        if (!ok) break;
+#pragma unroll 2
+        for (int n = rank; n < nt; n += a.C) {
+          float v[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) v[k] = k < a.C ? ld_on(so + n * 128, k) : 0.f;
+          finish(((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7])), n);
+        }
+      }
+    }
+    if (!ok && lane == 0 && !*abort_flag) {
+      *abort_flag = 1;
+      report_error(g_linear_status, MOE_ERR_TIMEOUT, 83);
+    }
+  }
+
+  __syncwarp();
+  tc_fence_before();
+  if (a.C > 1) cluster_sync();               // no CTA leaves while another reads its sums
+  else __syncthreads();
+  if (warp == kWarpMma) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
+  }
+}
+
+template <int FMT, bool HALF>
+cudaError_t launch_one(const TcArgs& a, const CUtensorMap& tm, int grid, size_t smem, cudaStream_t s) {
+  return launch_cluster(linear_tc_kernel<FMT, HALF>, a.C, grid, kThreads, smem, s, a, tm);
+}
+
+size_t tc_smem(int nraw, int cpr, int np, int C) {
+  return 1024 + size_t(nraw) * kRawBytes + size_t(cpr) * 2 * np * 128 + (C > 1 ? size_t(2) * np * 512 : 0) + kBars +
+         256 * 4 + 64 * 4 + size_t(np) * kWarps * 4;
+}
+
+}  // namespace
+
+cudaError_t linear_status(int* out) {
+  cudaError_t e = cudaMemcpyFromSymbol(out, g_linear_status, sizeof(g_linear_status));
+  const int zero[2] = {0, 0};
+  if (e == cudaSuccess && out[0] != 0) e = cudaMemcpyToSymbol(g_linear_status, zero, sizeof(zero));
+  return e;
+}
+
+TcPlan plan_linear_tc(int N, int K, int T, int num_sms) {
+  TcPlan best{};
+  best.cost = -1;
+  const int stages = (K + 127) / 128, tiles = (N + 127) / 128;
+  for (int C = 1; C <= 8; C *= 2) {
+    TcPlan p{};
+    p.C = C;
+    p.cpr = (stages + C - 1) / C;
+    if (C > 1 && (C - 1) * p.cpr >= stages) continue;
+    const int at_once = clusters_at_once(C, num_sms);
+    for (int np = min(64, (T + 15) / 16 * 16); np >= 16; np -= 16) {
+      if (tc_smem(4, p.cpr, np, C) > kMaxSmem) continue;
+      p.ny = (T + np - 1) / np;
+      p.tt = (T + p.ny - 1) / p.ny;
+      p.np = (p.tt + 15) / 16 * 16;
+      for (p.nraw = kMaxRaw; tc_smem(p.nraw, p.cpr, p.np, C) > kMaxSmem; --p.nraw) {}
+      p.smem = tc_smem(p.nraw, p.cpr, p.np, C);
+      p.ctas = min(tiles, max(1, at_once / p.ny));
+      const int waves = (p.ny * p.ctas + at_once - 1) / at_once, per = (tiles + p.ctas - 1) / p.ctas;
+      // cycles, fitted to measured calls: launch, converting the activations,
+      // 600 a stage of a CTA's tiles; a cluster joins a tile in 3900 and 155
+      // more for each token, under the next tile's stages
+      const double tile = p.cpr * 600.0, join = C > 1 ? 3900.0 + 155 * p.np : 100.0 * p.np;
+      p.cost = waves * ((C > 1 ? 7500.0 : 2500.0) + p.np * double(p.cpr) * 128 * 0.25 + per * (tile > join ? tile : join) +
+                        join);
+      if (best.cost < 0 || p.cost < best.cost) best = p;
+      break;
+    }
+  }
+  return best;
+}
+
+cudaError_t launch_linear_tc(const LinearCall& c, const TcPlan& p, cudaStream_t s) {
+  TcArgs a{};
+  a.scales = c.scales; a.row_scales = c.row_scales; a.bias = c.bias; a.x = c.x; a.y = c.y;
+  a.N = c.rows; a.K = c.cols; a.T = c.T;
+  a.spr = c.cols / c.block;
+  a.stages = (c.cols + 127) / 128;
+  a.C = p.C; a.cpr = p.cpr; a.ny = p.ny; a.tt = p.tt; a.np = p.np; a.nraw = p.nraw;
+  a.x_type = c.x_type; a.y_type = c.y_type; a.gated = c.gated;
+  CUtensorMap tm;
+  if (!make_map(&tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, c.codes, uint64_t(a.K) / 2, uint64_t(a.N), 64, 128,
+                CU_TENSOR_MAP_SWIZZLE_64B))
+    return cudaErrorInvalidValue;
+  const int grid = p.C * p.ny * p.ctas;
+  if (c.scale_fmt == 1) return launch_one<F_E32, false>(a, tm, grid, p.smem, s);
+  if (c.block == 128)
+    return c.half_levels ? launch_one<F_H128, true>(a, tm, grid, p.smem, s) : launch_one<F_H128, false>(a, tm, grid, p.smem, s);
+  return c.half_levels ? launch_one<F_H32, true>(a, tm, grid, p.smem, s) : launch_one<F_H32, false>(a, tm, grid, p.smem, s);
+}
+
+}  // namespace moe

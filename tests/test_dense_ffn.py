@@ -112,6 +112,8 @@ SHAPES = [
     (128, 128, 64), (129, 136, 72), (257, 512, 1000), (300, 2048, 768),
     # wide tiles: full, and ragged in every direction
     (512, 2048, 4096), (1111, 1000, 3144), (2049, 2056, 1032),
+    # a tile's reduction split over a cluster: by 4 and 2 on narrow tiles, over two pairs on wide ones, uneven parts
+    (5, 1032, 520), (100, 2048, 256), (130, 776, 1096), (777, 2056, 5000), (500, 1024, 4104),
 ]
 
 
