@@ -364,6 +364,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ffn_gemm_kernel(const __grid_
   if (a.reset && blockIdx.x == 0 && threadIdx.x == 0) { a.status[0] = 0; a.status[1] = 0; }
 
   const int unit = int(blockIdx.x) / (CG * split), units = int(gridDim.x) / (CG * split);
+  // Round by round, every other one backwards: the list is sorted by depth, so
+  // who had a deep tile gets a shallow one next.
+  auto turn = [&](int round) { return round * units + ((round & 1) ? units - 1 - unit : unit); };
   auto find = [&](int t, int* m, int* n) -> int {
     int i = 0;
     while (i + 1 < a.n && t >= a.p[i + 1].tile0) ++i;
@@ -376,7 +379,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ffn_gemm_kernel(const __grid_
     Cursor<T::STAGES> c;
     const uint32_t ring = smem_u32(base), leader = CG == 1 ? smem_u32(full) : in_leader(full);
     bool ok = true;
-    for (int t = unit; t < a.ntiles && ok; t += units) {
+    for (int tc = 0, t; (t = turn(tc)) < a.ntiles && ok; ++tc) {
       int m, n;
       const int i = find(t, &m, &n);
       const Problem& p = a.p[i];
@@ -394,9 +397,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ffn_gemm_kernel(const __grid_
     // --------------------------------------------------------- issuer
     Cursor<T::STAGES> c;
     const uint32_t ring = smem_u32(base);
-    int tc = 0;
     bool ok = true;
-    for (int t = unit; t < a.ntiles && ok; t += units, ++tc) {
+    for (int tc = 0, t; (t = turn(tc)) < a.ntiles && ok; ++tc) {
       int m, n;
       const Problem& p = a.p[find(t, &m, &n)];
       const int buf = tc & 1;
@@ -416,8 +418,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ffn_gemm_kernel(const __grid_
     // ------------------------------------------------------- epilogue
     const int q = warp & 3, half = warp >> 2;
     constexpr int HC = BN / 2;                     // columns of this warp
-    int tc = 0;
-    for (int t = unit; t < a.ntiles; t += units, ++tc) {
+    for (int tc = 0, t; (t = turn(tc)) < a.ntiles; ++tc) {
       int m, n;
       const Problem& p = a.p[find(t, &m, &n)];
       const int buf = tc & 1;
@@ -777,11 +778,11 @@ struct Operands {
 int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
 // CTAs (or pairs, cg = 2) that share one tile's reduction: as many of `most` (4
-// or 2) as leave every tile its own cluster on the machine and each part three
-// stages.
+// or 2) as let all tiles' clusters run at once (33 clusters of 4, not 37: a 34th
+// would start when the first ends) and give each part three stages.
 int split_of(int tiles, int kblocks, int cg, int most, int num_sms) {
   for (int s = most; s > 1; s /= 2)
-    if (tiles * s * cg <= num_sms / 8 * 8 && kblocks >= 3 * s && (s - 1) * ceil_div(kblocks, s) < kblocks) return s;
+    if (tiles <= clusters_at_once(s * cg, num_sms) && kblocks >= 3 * s && (s - 1) * ceil_div(kblocks, s) < kblocks) return s;
   return 1;
 }
 // Cycles of one product on tiles of `step` cycles per 64-deep step; joining a
