@@ -565,8 +565,8 @@ struct Plan {
 
 // The launch that ends first by a rough count of cycles, fitted to measured
 // calls (40000 x 2048: 8, 16, 32, 64 tokens 17.6, 33, 64 and 98 cycles a block
-// of 16 x 32): converting a CTA's activations, its share of the blocks, or a
-// warp's own chain of stages where there are few.
+// of 16 x 32): converting a CTA's activations, its share of the blocks, and
+// half of a warp's own chain of stages, which the others cover in part.
 Plan plan_linear(int N, int nb, int T, int num_sms) {
   Plan best{};
   best.cost = -1;
@@ -603,7 +603,7 @@ Plan plan_linear(int N, int nb, int T, int num_sms) {
         const double block = 6 + 13.5 * NT, stage = 250 + CB * (25 + 15 * NT);
         const double thr = per * (double(p.cpr) * CB * block + 60 + KG * (10 + 4 * NT));
         const double lat = rounds * (stages * stage + 200 + (C > 1 ? 100 : 0));
-        p.cost = waves * (5000 + p.tt * double(p.cpr) * CB * 32 * 0.1 + (C > 1 ? 2500 : 0) + (thr > lat ? thr : lat));
+        p.cost = waves * (5000 + p.tt * double(p.cpr) * CB * 32 * 0.1 + (C > 1 ? 2500 : 0) + thr + 0.5 * lat);
         if (best.cost < 0 || p.cost < best.cost) best = p;
       }
     }
