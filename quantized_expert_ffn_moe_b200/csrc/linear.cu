@@ -661,9 +661,9 @@ cudaError_t launch_linear(const LinearCall& c, int num_sms, cudaStream_t s) {
     en = Entry{a.N, a.nb, a.T, num_sms, plan_linear(a.N, a.nb, a.T, num_sms), plan_linear_tc(a.N, a.K, a.T, num_sms)};
   const Plan& p = en.p;
   // more than one group of 8 tokens and results of 16 bits: the tensor-core
-  // form where its count is clearly the smaller one (32 tokens: 40000 x 2048 26
-  // against 41 us, 2048 x 2048 12 against 9 us)
-  if (c.y_type != MOE_FP32 && c.T > 8 && en.tc.cost >= 0 && (p.cost < 0 || en.tc.cost < 0.85 * p.cost))
+  // form where its count is the smaller one (32 tokens: 40000 x 2048 25 against
+  // 41 us, 768 x 2048 7.9 against 7.7 us)
+  if (c.y_type != MOE_FP32 && c.T > 8 && en.tc.cost >= 0 && (p.cost < 0 || en.tc.cost < 0.95 * p.cost))
     return launch_linear_tc(c, en.tc, s);
   if (p.cost < 0) return cudaErrorInvalidConfiguration;
   a.chunks = p.chunks; a.C = p.C; a.cpr = p.cpr; a.KG = p.KG; a.groups = p.groups; a.ny = p.ny; a.tt = p.tt;

@@ -70,9 +70,10 @@ __device__ __forceinline__ uint32_t on_rank(const void* p, int rank) {
 __device__ __forceinline__ void arrive_on(uint64_t* bar, int rank) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(on_rank(bar, rank)) : "memory");
 }
-__device__ __forceinline__ float ld_on(const float* p, int rank) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(on_rank(p, rank)));
+__device__ __forceinline__ float4 ld_on(const float* p, int rank) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(on_rank(p, rank)));
   return v;
 }
 // mbar_wait that also sees what the cluster's CTAs wrote before they arrived.
@@ -166,14 +167,27 @@ struct StageScales {
   }
 };
 
+__device__ __forceinline__ uint32_t pack16(float a, float b, bool bf) {
+  if (bf) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  }
+  return h2_as_u32(__floats2half2_rn(a, b));
+}
+// Values of rows row to row + 3, the last row's where there is none.
+__device__ __forceinline__ float4 row4(const float* p, int row, int N) {
+  return make_float4(__ldg(p + min(row, N - 1)), __ldg(p + min(row + 1, N - 1)), __ldg(p + min(row + 2, N - 1)),
+                     __ldg(p + min(row + 3, N - 1)));
+}
+
 template <int FMT, bool HALF>
 __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const TcArgs a, const __grid_constant__ CUtensorMap tm) {
   extern __shared__ __align__(1024) unsigned char csm_raw[];
   unsigned char* base = csm_raw + ((0u - smem_u32(csm_raw)) & 1023u);
   unsigned char* sraw = base;                                           // [nraw] stages of codes
   unsigned char* sx = sraw + a.nraw * kRawBytes;                        // [2 cpr] blocks of 64 columns: [np] rows of 128 bytes
-  float* sout = reinterpret_cast<float*>(sx + size_t(a.cpr) * 2 * a.np * 128);   // C > 1: [2][np][128]
-  uint64_t* bars = reinterpret_cast<uint64_t*>(sout + (a.C > 1 ? 2 * a.np * 128 : 0));
+  float* sout = reinterpret_cast<float*>(sx + size_t(a.cpr) * 2 * a.np * 128);   // sums of a tile, [2][np][128 rows]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sout + 2 * a.np * 128);
   uint64_t* full_raw = bars;
   uint64_t* empty_raw = full_raw + kMaxRaw;
   uint64_t* full_a = empty_raw + kMaxRaw;
@@ -307,7 +321,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const TcArgs a, 
     const bool bf = a.x_type == MOE_BF16;
     const uint16_t* xb = static_cast<const uint16_t*>(a.x) + size_t(t0) * a.K + col0;
     const int sl = nt >= kWarps ? 1 : kWarps / nt, units = nt * sl, per = (W + sl - 1) / sl;
-    constexpr int HOLD = 14;
+    constexpr int HOLD = 8;
     // one unit a warp and HOLD words a lane: kept between the two passes
     const bool held = units <= kWarps && per <= HOLD * 32;
     uint4 v[HOLD];
@@ -507,38 +521,31 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const TcArgs a, 
   } else {
     // ------------------------------------------------------- results
     bool ok = true;
+    const bool out_bf = a.y_type == MOE_BF16;
+    // four values (two when gated) of every token start on 8 (4) bytes
+    const bool wide_out = a.N % 4 == 0;
     for (int i = 0; i < my_tiles; ++i) {
       const int buf = i & 1;
       const uint32_t top = row_top(i + 2);         // its loads end under this tile's products
       ok = __all_sync(0xffffffffu, mbar_wait(&acc_full[buf], (i >> 1) & 1, abort_flag));
       if (!ok) break;
       tc_fence_after();
-      const int row0 = (cta + i * ctas) * 128, row = row0 + r;
+      const int row0 = (cta + i * ctas) * 128;
       const float down = buf ? inv_norm[1] : inv_norm[0];
-      const float rs = FMT == F_E32 ? __ldg(a.row_scales + min(row, a.N - 1)) : 1.f;
-      const float bias = a.bias ? __ldg(a.bias + min(row, a.N - 1)) : 0.f;
-      // one token's result of this lane's row (of its pair of rows when gated)
-      auto finish = [&](float v, int n) {
-        v *= rs;
-        if (!a.gated) {
-          if (row < a.N) store_as(a.y, a.y_type, size_t(t0 + n) * a.N + row, v + bias);
-        } else {
-          const float other = __shfl_xor_sync(0xffffffffu, v, 1);
-          if (!(lane & 1) && row < a.N)
-            store_as(a.y, a.y_type, size_t(t0 + n) * (a.N >> 1) + (row >> 1), v / (1.f + expf(-v)) * other);
-        }
-      };
-      float* so = sout + buf * a.np * 128 + r;
+      // the sums into shared memory, one token's 128 rows next to each other
+      float* so = sout + buf * a.np * 128;
 #pragma unroll 1
-      for (int n0 = 0; n0 < nt; n0 += 16) {
+      for (int n0 = 0; n0 < a.np; n0 += 16) {
         uint32_t v[16];
         ld16(tmem + (uint32_t(q * 32) << 16) + uint32_t(buf * 64 + n0), v);
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          if (n0 + j >= nt) break;
-          const float f = __uint_as_float(v[j]) * down * sinv[n0 + j];
-          if (a.C == 1) finish(f, n0 + j);
-          else so[(n0 + j) * 128] = f;
+        for (int j = 0; j < 16; j += 4) {
+          const float4 iv = *reinterpret_cast<const float4*>(sinv + n0 + j);
+          float* at = so + (n0 + j) * 128 + r;
+          at[0] = __uint_as_float(v[j]) * down * iv.x;
+          at[128] = __uint_as_float(v[j + 1]) * down * iv.y;
+          at[256] = __uint_as_float(v[j + 2]) * down * iv.z;
+          at[384] = __uint_as_float(v[j + 3]) * down * iv.w;
         }
       }
       tc_fence_before();
@@ -558,12 +565,53 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const TcArgs a, 
         __syncwarp();
         ok = __all_sync(0xffffffffu, wait_cluster(&joined[buf], (i >> 1) & 1, abort_flag));
         if (!ok) break;
-#pragma unroll 2
-        for (int n = rank; n < nt; n += a.C) {
-          float v[8];
+      } else {
+        named_bar_sync(1, 128);
+      }
+      // Tokens dealt to the ranks and their warps: a lane adds four rows of one
+      // and stores them at once.  (A lane per row and a store per value cost
+      // the issue slots that the dequantising warps need: 15 of 50 us at 64
+      // tokens x 20480 x 4096.)
+      const int row = row0 + lane * 4;
+      float4 rs = make_float4(1.f, 1.f, 1.f, 1.f), bias = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (FMT == F_E32) rs = row4(a.row_scales, row, a.N);
+      if (a.bias) bias = row4(a.bias, row, a.N);
+      for (int n = rank + a.C * q; n < nt; n += a.C * 4) {
+        const float* at = so + n * 128 + lane * 4;
+        float4 v[8];
 #pragma unroll
-          for (int k = 0; k < 8; ++k) v[k] = k < a.C ? ld_on(so + n * 128, k) : 0.f;
-          finish(((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7])), n);
+        for (int k = 0; k < 8; ++k) {
+          v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (k < a.C) v[k] = a.C > 1 ? ld_on(at, k) : *reinterpret_cast<const float4*>(at);
+        }
+        float4 f = v[0];
+#pragma unroll
+        for (int k = 1; k < 8; ++k) {
+          f.x += v[k].x; f.y += v[k].y; f.z += v[k].z; f.w += v[k].w;
+        }
+        f.x *= rs.x; f.y *= rs.y; f.z *= rs.z; f.w *= rs.w;
+        uint16_t* y = static_cast<uint16_t*>(a.y);
+        if (!a.gated) {
+          f.x += bias.x; f.y += bias.y; f.z += bias.z; f.w += bias.w;
+          const uint32_t lo = pack16(f.x, f.y, out_bf), hi = pack16(f.z, f.w, out_bf);
+          y += size_t(t0 + n) * a.N + row;
+          if (wide_out && row + 4 <= a.N) {
+            *reinterpret_cast<uint2*>(y) = make_uint2(lo, hi);
+          } else {
+            if (row < a.N) y[0] = uint16_t(lo);
+            if (row + 1 < a.N) y[1] = uint16_t(lo >> 16);
+            if (row + 2 < a.N) y[2] = uint16_t(hi);
+            if (row + 3 < a.N) y[3] = uint16_t(hi >> 16);
+          }
+        } else {
+          const uint32_t h = pack16(f.x / (1.f + __expf(-f.x)) * f.y, f.z / (1.f + __expf(-f.z)) * f.w, out_bf);
+          y += size_t(t0 + n) * (a.N >> 1) + (row >> 1);
+          if (wide_out && row + 4 <= a.N) {
+            *reinterpret_cast<uint32_t*>(y) = h;
+          } else {
+            if (row < a.N) y[0] = uint16_t(h);
+            if (row + 2 < a.N) y[1] = uint16_t(h >> 16);
+          }
         }
       }
     }
@@ -589,7 +637,7 @@ cudaError_t launch_one(const TcArgs& a, const CUtensorMap& tm, int grid, size_t 
 }
 
 size_t tc_smem(int nraw, int cpr, int np, int C) {
-  return 1024 + size_t(nraw) * kRawBytes + size_t(cpr) * 2 * np * 128 + (C > 1 ? size_t(2) * np * 512 : 0) + kBars +
+  return 1024 + size_t(nraw) * kRawBytes + size_t(cpr) * 2 * np * 128 + size_t(2) * np * 512 + kBars +
          256 * 4 + 64 * 4 + size_t(np) * kWarps * 4;
 }
 
@@ -621,12 +669,11 @@ TcPlan plan_linear_tc(int N, int K, int T, int num_sms) {
       p.smem = tc_smem(p.nraw, p.cpr, p.np, C);
       p.ctas = min(tiles, max(1, at_once / p.ny));
       const int waves = (p.ny * p.ctas + at_once - 1) / at_once, per = (tiles + p.ctas - 1) / p.ctas;
-      // cycles, fitted to measured calls: launch, converting the activations,
-      // 600 a stage of a CTA's tiles; a cluster joins a tile in 3900 and 155
-      // more for each token, under the next tile's stages
-      const double tile = p.cpr * 600.0, join = C > 1 ? 3900.0 + 155 * p.np : 100.0 * p.np;
-      p.cost = waves * ((C > 1 ? 7500.0 : 2500.0) + p.np * double(p.cpr) * 128 * 0.25 + per * (tile > join ? tile : join) +
-                        join);
+      // cycles, fitted to 60 measured calls of 16 to 64 tokens (6% rms): launch
+      // and the cluster's start, converting the activations, the stages of a
+      // CTA's tiles, their results
+      p.cost = waves * (2000.0 + (C > 1 ? 3200.0 : 0.0) + 0.188 * p.np * p.cpr * 128 + per * (459.0 * p.cpr + 2100.0 + 44.0 * p.np) +
+                        78.0 * p.np);
       if (best.cost < 0 || p.cost < best.cost) best = p;
       break;
     }
