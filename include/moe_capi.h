@@ -245,14 +245,17 @@ typedef enum moe_type { MOE_BF16 = 0, MOE_FP16 = 1, MOE_FP32 = 2 } moe_type;
  * formats).  x: [T][cols], x_type MOE_BF16 or MOE_FP16; y: [T][rows], y_type
  * any moe_type; bias: [rows] fp32 or NULL.  codes, scales, row_scales, x and y
  * are dense and 16-byte aligned; x and y may not overlap.  Any rows >= 1, any
- * T (meant for decode batches: T > 32 is cut into slices that each read the
- * weights); cols a multiple of the block, at most 32768.  Products and sums
- * are fp32, rounded once to y_type; the activations are taken exactly but for
- * elements smaller than 2^-27 of their row's largest magnitude, which are off
- * by at most 2^-38 of it.  A row of x that holds an infinity or a NaN gives a
- * row of NaN.  The call reads the weights before it waits for a kernel ahead
- * of it that lets its dependents launch early; none in this library writes
- * weights. */
+ * T (meant for decode batches: T > 64 is cut into slices that each read the
+ * weights); cols a multiple of the block, at most 32768.  Sums are fp32,
+ * rounded once to y_type.  The weights are taken exactly, but for results of
+ * 16 bits in batches of more than 8 tokens, where each may be rounded to fp16
+ * once (2^-11 of its value at most; E4M3 weights stay exact); the activations
+ * are taken exactly but for elements smaller than 2^-27 of their row's largest
+ * magnitude, which are off by at most 2^-38 of it.  A row of x that holds an
+ * infinity or a NaN gives a row of NaN.  The same call gives the same bits; a
+ * token's bits may depend on how many tokens it is multiplied with.  The call
+ * reads the weights before it waits for a kernel ahead of it that lets its
+ * dependents launch early; none in this library writes weights. */
 int moe_linear_forward(const moe_config* cfg, const uint8_t* codes, const void* scales, const float* row_scales,
                        int32_t rows, int32_t cols, const float* bias, const void* x, int32_t x_type, int32_t T,
                        void* y, int32_t y_type, void* stream);

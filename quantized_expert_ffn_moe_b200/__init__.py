@@ -308,29 +308,28 @@ def linear_config_of(bits=4, block=32, half_levels=False, fp8_scales=False) -> M
 
 _types = None        # torch dtype -> moe_type, filled by the first call (torch is imported then)
 _raw_stream = None   # device index -> handle of its current stream
+_current_device = None
 
 
 def _torch_types():
-    global _types, _raw_stream
+    global _types, _raw_stream, _current_device
     if _types is None:
         import torch
         _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
             lambda i: torch.cuda.current_stream(i).cuda_stream)
+        _current_device = torch.cuda.current_device
         _types = {torch.bfloat16: MOE_BF16, torch.float16: MOE_FP16, torch.float32: MOE_FP32}
     return _types
 
 
 def _dense(what: str, names: str, tensors) -> int:
-    """Every given tensor dense and on one CUDA device, whose index is
-    returned; the C entry sees only pointers."""
-    dev = None
+    """Every given tensor (the first always is) dense and on one CUDA device,
+    whose index is returned; the C entry sees only pointers."""
+    dev = tensors[0].get_device()
     for i, t in enumerate(tensors):
         if t is None:
             continue
-        d = t.get_device()
-        if dev is None:
-            dev = d
-        if d != dev or d < 0 or not t.is_contiguous():
+        if t.get_device() != dev or dev < 0 or not t.is_contiguous():
             name = names.split()[i]
             if not t.is_contiguous():
                 raise ValueError(f"{what}: {name} is not contiguous")
@@ -348,9 +347,8 @@ def _type_of(what: str, name: str, t, fp32: bool = False) -> int:
 def _on_device(dev: int, stream, entry, *args) -> int:
     """entry(*args, stream handle) with device `dev` current; without a stream,
     on that device's current stream."""
-    import torch
-    _torch_types()
-    if torch.cuda.current_device() != dev:
+    if _current_device() != dev:
+        import torch
         with torch.cuda.device(dev):
             return entry(*args, _raw_stream(dev) if stream is None else _stream(stream))
     return entry(*args, _raw_stream(dev) if stream is None else _stream(stream))
@@ -369,9 +367,10 @@ def _packed(what: str, cfg: MoeConfig, codes, scales, row_scales, rows: int, col
 
 def _linear(what: str, entry, cfg: MoeConfig, codes, scales, row_scales, bias, x, y, per_out: int, stream, check) -> int:
     """Both packed products: per_out rows of the matrix for each output column."""
-    if x.dim() != 2 or y.dim() != 2 or x.shape[0] != y.shape[0]:
-        raise ValueError(f"{what}: x is {tuple(x.shape)}, the output {tuple(y.shape)}")
-    (T, cols), out = x.shape, y.shape[1]
+    xs, ys = x.shape, y.shape
+    if len(xs) != 2 or len(ys) != 2 or xs[0] != ys[0]:
+        raise ValueError(f"{what}: x is {tuple(xs)}, the output {tuple(ys)}")
+    T, cols, out = xs[0], xs[1], ys[1]
     _packed(what, cfg, codes, scales, row_scales, per_out * out, cols)
     xt, yt = _type_of(what, "x", x), _type_of(what, "the output", y, fp32=True)
     head = (ctypes.byref(cfg), codes.data_ptr(), scales.data_ptr(), _ptr(row_scales), out, cols)

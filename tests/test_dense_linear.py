@@ -138,7 +138,7 @@ def half_step(t):
 CASES = [
     # T, rows, cols: every token group size, ragged rows, one block, columns off the stage and the copy width
     (1, 1, 32), (1, 16, 64), (2, 17, 96), (3, 15, 128), (5, 33, 160), (8, 256, 256), (1, 2048, 2048), (7, 100, 2080),
-    (9, 48, 1056), (16, 130, 4096), (17, 64, 4128), (32, 31, 2048), (33, 50, 512), (64, 77, 8192), (100, 40, 1024), (48, 300, 544), (10, 700, 4096), (16, 150000, 128),
+    (9, 48, 1056), (16, 130, 4096), (17, 64, 4128), (32, 31, 2048), (33, 50, 512), (64, 77, 8192), (100, 40, 1024), (48, 300, 544), (10, 700, 4096), (16, 150000, 128), (12, 40, 32), (1000, 64, 512), (64, 20481, 1056),
     (1, 3000, 768), (4, 40, 32768),
 ]
 
