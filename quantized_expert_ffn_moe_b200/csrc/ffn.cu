@@ -13,7 +13,10 @@
 // h and dgu = (dg, du) from their epilogue; then dx, dWgu and dWd as one list
 // of tiles).  g, u, dh and every sum stay fp32; h and dgu are rounded to 16
 // bits once because they are operands of the next tensor-core product, which
-// adds an error of the size of the output's own rounding.  Recomputing g and u
+// adds an error of the size of the output's own rounding.  Batches of up to 64
+// tokens, where that error is the same few roundings in every output, do not
+// pay it: a tile has 128 rows anyway, so row 64 + t holds what the rounding of
+// row t left (another 8 or 11 bits), and the products of both are added.  Recomputing g and u
 // instead of storing them costs 4 of the 16 T H I products and saves 8 bytes
 // of fp32 a token and column; 16-bit copies of them would add their rounding
 // to every gradient.
@@ -33,6 +36,7 @@ namespace moe {
 
 namespace {
 
+constexpr int kRest = 64;                        // batches of up to this many tokens keep the rest of a rounding
 constexpr int BK = 64;                           // reduction depth of a stage: one 128-byte swizzle row
 constexpr int kAStage = 128 * 128;               // 128 rows x 64 deep x 2 bytes
 constexpr int kMaxStages = 8;
@@ -55,6 +59,9 @@ struct Problem {
   int M, N, kblocks;
   int tiles_m, tiles_n, tile0;
   int a_mn, b_mn;
+  int a_step, b_step;    // the operands' coordinate along the reduction: BK a step, 0 to take the same 64 again
+  int rest;              // EPI_GATED: what the rounding of a row leaves goes kRest rows further down
+  int fold;              // rows kRest further down are added to a row (one tile per CTA)
   void* out;
   int ld;
 };
@@ -203,13 +210,14 @@ __device__ __forceinline__ void load_operand(uint32_t dst, const CUtensorMap* ma
 template <int CG, bool AMN, bool BMN, int BROWS, int STAGE, int STAGES>
 __device__ __forceinline__ bool load_steps(uint32_t ring, uint64_t* full, uint64_t* empty, uint32_t full_leader, int rank,
                                            Cursor<STAGES>& c, const CUtensorMap* ma, const CUtensorMap* mb, int row_a,
-                                           int row_b, int kb0, int steps, const volatile int* abort_flag) {
+                                           int row_b, int a_step, int b_step, int kb0, int steps,
+                                           const volatile int* abort_flag) {
   for (int kb = kb0; kb < kb0 + steps; ++kb) {
     if (!mbar_wait(&empty[c.s], c.parity ^ 1u, abort_flag)) return false;
     if (rank == 0) mbar_arrive_expect_tx(&full[c.s], CG * (kAStage + BROWS * 128));
     const uint32_t st = ring + uint32_t(c.s) * STAGE, bar = full_leader + uint32_t(c.s) * 8;
-    load_operand<CG, AMN, 128>(st, ma, row_a, kb * BK, bar);
-    load_operand<CG, BMN, BROWS>(st + kAStage, mb, row_b, kb * BK, bar);
+    load_operand<CG, AMN, 128>(st, ma, row_a, kb * a_step, bar);
+    load_operand<CG, BMN, BROWS>(st + kAStage, mb, row_b, kb * b_step, bar);
     c.next();
   }
   return true;
@@ -304,6 +312,11 @@ __device__ __forceinline__ void store16(uint16_t* row, int n, int cols, const fl
 __device__ __forceinline__ void store4(uint16_t* row, int n, int cols, float a, float b, float c, float d, int bf16) {
   if (n < cols) *reinterpret_cast<uint2*>(row + n) = make_uint2(pack2(a, b, bf16), pack2(c, d, bf16));
 }
+// What rounding to 16 bits leaves of a value.
+__device__ __forceinline__ float rest_of(float v, int bf16) {
+  const float r = bf16 ? __bfloat162float(__float2bfloat16_rn(v)) : __half2float(__float2half_rn(v));
+  return isfinite(r) ? v - r : 0.f;
+}
 // All rows of [][ld] start on 32 bytes.
 __device__ __forceinline__ bool on_32(const void* p, int ld) {
   return (reinterpret_cast<uintptr_t>(p) & 31) == 0 && (ld & 15) == 0;
@@ -387,7 +400,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ffn_gemm_kernel(const __grid_
       const Part kp = part_of(p.kblocks, split, srank);
       auto run = [&](auto amn, auto bmn) {
         return load_steps<CG, amn.value, bmn.value, T::BROWS, T::STAGE, T::STAGES>(
-            ring, full, empty, leader, rank, c, &maps.a[i], &maps.b[i], row_a, row_b, kp.first, kp.steps, abort_flag);
+            ring, full, empty, leader, rank, c, &maps.a[i], &maps.b[i], row_a, row_b, p.a_step, p.b_step, kp.first, kp.steps,
+            abort_flag);
       };
       ok = p.a_mn ? run(Yes(), Yes()) : p.b_mn ? run(No(), Yes()) : run(No(), No());
     }
@@ -429,14 +443,14 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ffn_gemm_kernel(const __grid_
       }
       tc_fence_after();
       const int row = m * T::BM + rank * 128 + q * 32 + lane;
-      if (split > 1) {
-        // this CTA's partial sums for the others, over its ring: all copies
-        // have been used
+      if (split > 1 || p.fold) {
+        // this CTA's partial sums for the others and for the rows they are
+        // added to, over its ring: all copies have been used
 #pragma unroll
         for (int c = 0; c < HC; c += 16) {
           uint32_t v[16];
           tmem_ld16(tmem + (uint32_t(q * 32) << 16) + uint32_t(buf * BN + half * HC + c), v);
-          if (row < p.M) {
+          if ((p.fold ? row % kRest : row) < p.M) {
 #pragma unroll
             for (int j = 0; j < 16; j += 4)
               *partial(base, half * HC + c + j, q * 32 + lane) =
@@ -471,6 +485,11 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ffn_gemm_kernel(const __grid_
               f[j] = g * sigmoid(g) * u;
             }
             store16(out, col >> 1, p.ld, f, a.bf16, wide);
+            if (p.rest) {
+#pragma unroll
+              for (int j = 0; j < 16; ++j) f[j] = rest_of(f[j], a.bf16);
+              store16(out + size_t(kRest) * p.ld, col >> 1, p.ld, f, a.bf16, wide);
+            }
           }
         }
       }
@@ -481,27 +500,38 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ffn_gemm_kernel(const __grid_
   }
 
   __syncwarp();
-  if (split > 1) {
+  int join_m = 0, join_n = 0, join_p = 0;
+  if (unit < a.ntiles) join_p = find(unit, &join_m, &join_n);
+  if (split > 1 || a.p[join_p].fold) {
     // Every CTA of the cluster finishes its share of the tile's columns.
     cluster_sync();
     if (warp < kEpiWarps && !*abort_flag) {
-      int m, n;
-      const Problem& p = a.p[find(unit, &m, &n)];
-      const int q = warp & 3, half = warp >> 2, row = m * T::BM + rank * 128 + q * 32 + lane;
-      const int cols = BN / split / 2, c0 = srank * (BN / split) + half * cols;       // 8, 16 or 64
+      const Problem& p = a.p[join_p];
+      const int q = warp & 3, half = warp >> 2, place = q * 32 + lane, row = join_m * T::BM + rank * 128 + place;
+      const int cols = BN / split / 2, c0 = srank * (BN / split) + half * cols;       // 8, 16, 32 or 64
       if (row < p.M) {
         uint16_t* out = static_cast<uint16_t*>(p.out) + size_t(row) * p.ld;
 #pragma unroll 2
         for (int c = c0; c < c0 + cols; c += 8) {
-          const float4 v = sum_parts(partial(base, c, q * 32 + lane), split, rank, CG);
-          const float4 w = sum_parts(partial(base, c + 4, q * 32 + lane), split, rank, CG);
-          const int col = n * BN + c;
+          float4 v = sum_parts(partial(base, c, place), split, rank, CG);
+          float4 w = sum_parts(partial(base, c + 4, place), split, rank, CG);
+          if (p.fold) {
+            const float4 r = sum_parts(partial(base, c, place + kRest), split, rank, CG);
+            const float4 s = sum_parts(partial(base, c + 4, place + kRest), split, rank, CG);
+            v.x += r.x; v.y += r.y; v.z += r.z; v.w += r.w;
+            w.x += s.x; w.y += s.y; w.z += s.z; w.w += s.w;
+          }
+          const int col = join_n * BN + c;
           if (EPI == EPI_STORE) {
             store4(out, col, p.ld, v.x, v.y, v.z, v.w, a.bf16);
             store4(out, col + 4, p.ld, w.x, w.y, w.z, w.w, a.bf16);
           } else {
-            store4(out, col >> 1, p.ld, v.x * sigmoid(v.x) * v.y, v.z * sigmoid(v.z) * v.w, w.x * sigmoid(w.x) * w.y,
-                   w.z * sigmoid(w.z) * w.w, a.bf16);
+            const float h[4] = {v.x * sigmoid(v.x) * v.y, v.z * sigmoid(v.z) * v.w, w.x * sigmoid(w.x) * w.y,
+                                w.z * sigmoid(w.z) * w.w};
+            store4(out, col >> 1, p.ld, h[0], h[1], h[2], h[3], a.bf16);
+            if (p.rest)
+              store4(out + size_t(kRest) * p.ld, col >> 1, p.ld, rest_of(h[0], a.bf16), rest_of(h[1], a.bf16),
+                     rest_of(h[2], a.bf16), rest_of(h[3], a.bf16), a.bf16);
           }
         }
       }
@@ -523,6 +553,8 @@ struct GradArgs {
   int tiles_m, tiles_n, kblocks;      // kblocks of one phase (the reduction over H)
   int bf16, reset;
   int split;                          // narrow tile: CTAs of a cluster that share the reductions
+  int rest;                           // T <= kRest: h and dgu have 2 kRest rows, the second half the rest of the
+                                      // rounding; rows without a token are 0 (they are reduced over)
   uint16_t* h;                        // [T][I], or null
   uint16_t* dgu;                      // [T][2I]
   int* status;
@@ -583,6 +615,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) ffn_grad_kernel(const __grid_
 
   const int unit = int(blockIdx.x) / (CG * split), units = int(gridDim.x) / (CG * split);
   const int ntiles = a.tiles_m * a.tiles_n;
+  const int rows = a.rest ? kRest : a.T;          // of h and dgu that are written (and as many of the rest)
   Problem shape{};
   shape.tiles_m = a.tiles_m;
   shape.tiles_n = a.tiles_n;
@@ -596,10 +629,10 @@ __global__ void __launch_bounds__(kGradThreads, 1) ffn_grad_kernel(const __grid_
       tile_of(shape, t, &m, &n);
       const int row_a = m * T::BM + rank * 128;
       ok = load_steps<CG, false, false, T::BROWS, T::STAGE, T::STAGES>(ring, full, empty, leader, rank, c, &tm_x, &tm_wgu,
-                                                                      row_a, n * 2 * NI + rank * T::BROWS, kp.first, kp.steps,
-                                                                      abort_flag) &&
+                                                                      row_a, n * 2 * NI + rank * T::BROWS, BK, BK, kp.first,
+                                                                      kp.steps, abort_flag) &&
            load_steps<CG, false, true, DROWS, T::STAGE, T::STAGES>(ring, full, empty, leader, rank, c, &tm_dy, &tm_wd,
-                                                                  row_a, n * NI + rank * DROWS, kp.first, kp.steps,
+                                                                  row_a, n * NI + rank * DROWS, BK, BK, kp.first, kp.steps,
                                                                   abort_flag);
     }
     if (!ok) { *abort_flag = 1; report_error(a.status, MOE_ERR_TIMEOUT, 60); }
@@ -682,7 +715,18 @@ __global__ void __launch_bounds__(kGradThreads, 1) ffn_grad_kernel(const __grid_
             fg[c + e + j] = u * fmaf(act, 1.f - s, s);
           }
         }
-        if (a.h && row < a.T) store16(a.h + size_t(row) * a.I, i0 + c, a.I, hv, a.bf16, h_wide);
+        if (a.h && row < rows) {
+          if (row >= a.T) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) hv[j] = 0.f;
+          }
+          store16(a.h + size_t(row) * a.I, i0 + c, a.I, hv, a.bf16, h_wide);
+          if (a.rest) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) hv[j] = rest_of(hv[j], a.bf16);
+            store16(a.h + size_t(row + kRest) * a.I, i0 + c, a.I, hv, a.bf16, h_wide);
+          }
+        }
       }
       tc_fence_before();
       __syncwarp();
@@ -697,17 +741,22 @@ __global__ void __launch_bounds__(kGradThreads, 1) ffn_grad_kernel(const __grid_
       for (int c = 0; c < PI; c += 16) {
         uint32_t v[16];
         tmem_ld16(tq + uint32_t(2 * NI + buf * NI + part * PI + c), v);
-        if (row < a.T) {
+        if (row < rows) {
 #pragma unroll
           for (int e = 0; e < 16; e += 8) {
             float d[16];
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
               const float dh = __uint_as_float(v[e + j]);
-              d[2 * j] = dh * fg[c + e + j];
-              d[2 * j + 1] = dh * fu[c + e + j];
+              d[2 * j] = row < a.T ? dh * fg[c + e + j] : 0.f;
+              d[2 * j + 1] = row < a.T ? dh * fu[c + e + j] : 0.f;
             }
             store16(a.dgu + size_t(row) * 2 * a.I, 2 * (i0 + c + e), 2 * a.I, d, a.bf16, dgu_wide);
+            if (a.rest) {
+#pragma unroll
+              for (int j = 0; j < 16; ++j) d[j] = rest_of(d[j], a.bf16);
+              store16(a.dgu + size_t(row + kRest) * 2 * a.I, 2 * (i0 + c + e), 2 * a.I, d, a.bf16, dgu_wide);
+            }
           }
         }
       }
@@ -727,7 +776,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) ffn_grad_kernel(const __grid_
       tile_of(shape, unit, &m, &n);
       const int q = warp & 3, part = warp >> 2, row = m * T::BM + q * 32 + lane;
       const int per = NI / split / 4, e0 = srank * (NI / split) + part * per;          // 4 or 8
-      if (row < a.T) {
+      if (row < rows) {
         for (int e = e0; e < e0 + per; e += 4) {
           const float4 p0 = sum_parts(partial(base, 2 * e, q * 32 + lane), split, 0, 1);
           const float4 p1 = sum_parts(partial(base, 2 * e + 4, q * 32 + lane), split, 0, 1);
@@ -737,15 +786,25 @@ __global__ void __launch_bounds__(kGradThreads, 1) ffn_grad_kernel(const __grid_
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const float g = gu[2 * j], u = gu[2 * j + 1], s = sigmoid(g), act = g * s;
-            h[j] = act * u;
-            d[2 * j] = dh[j] * (u * fmaf(act, 1.f - s, s));
-            d[2 * j + 1] = dh[j] * act;
+            h[j] = row < a.T ? act * u : 0.f;
+            d[2 * j] = row < a.T ? dh[j] * (u * fmaf(act, 1.f - s, s)) : 0.f;
+            d[2 * j + 1] = row < a.T ? dh[j] * act : 0.f;
           }
           const int i = n * NI + e;
           if (a.h) store4(a.h + size_t(row) * a.I, i, a.I, h[0], h[1], h[2], h[3], a.bf16);
           uint16_t* out = a.dgu + size_t(row) * 2 * a.I;
           store4(out, 2 * i, 2 * a.I, d[0], d[1], d[2], d[3], a.bf16);
           store4(out, 2 * i + 4, 2 * a.I, d[4], d[5], d[6], d[7], a.bf16);
+          if (a.rest) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) h[j] = rest_of(h[j], a.bf16);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) d[j] = rest_of(d[j], a.bf16);
+            if (a.h) store4(a.h + size_t(row + kRest) * a.I, i, a.I, h[0], h[1], h[2], h[3], a.bf16);
+            out += size_t(kRest) * 2 * a.I;
+            store4(out, 2 * i, 2 * a.I, d[0], d[1], d[2], d[3], a.bf16);
+            store4(out, 2 * i + 4, 2 * a.I, d[4], d[5], d[6], d[7], a.bf16);
+          }
         }
       }
     }
@@ -826,7 +885,9 @@ cudaError_t launch_gemm(GemmArgs& a, const Operands* op, int num_sms, cudaStream
   }
   for (int i = a.n; i < 3; ++i) { maps.a[i] = maps.a[0]; maps.b[i] = maps.b[0]; }
   a.split = a.n == 1 ? split_of(a.ntiles, a.p[0].kblocks, CG, CG == 1 ? 4 : 2, num_sms) : 1;
-  const int units = a.split > 1 ? a.ntiles : min(num_sms / CG, a.ntiles), cluster = CG * a.split;
+  bool single = a.split > 1;               // one tile per CTA or cluster
+  for (int i = 0; i < a.n; ++i) single = single || a.p[i].fold;
+  const int units = single ? a.ntiles : min(num_sms / CG, a.ntiles), cluster = CG * a.split;
   return launch_cluster(ffn_gemm_kernel<CG, BN, EPI>, cluster, units * cluster, kGemmThreads, T::SMEM, s, a, maps);
 }
 
@@ -855,8 +916,8 @@ cudaError_t launch_grad(GradArgs& a, const FfnCall& c, int num_sms, cudaStream_t
 struct FfnLayout {
   size_t status, h, dgu, total;
 };
-FfnLayout ffn_layout(int H, int I, int T, bool backward) {
-  (void)H;
+FfnLayout ffn_layout(int I, int tokens, bool backward) {
+  const int T = tokens < 2 * kRest ? 2 * kRest : tokens;       // rows of h and dgu: the rest of few tokens' roundings
   FfnLayout l{};
   l.status = 0;
   l.h = 256;
@@ -868,16 +929,17 @@ FfnLayout ffn_layout(int H, int I, int T, bool backward) {
 Problem problem(int M, int N, int K, int a_mn, int b_mn, void* out) {
   Problem p{};
   p.M = M; p.N = N; p.kblocks = ceil_div(K, BK); p.a_mn = a_mn; p.b_mn = b_mn; p.out = out; p.ld = N;
+  p.a_step = p.b_step = BK;
   return p;
 }
 
 }  // namespace
 
-size_t ffn_workspace_bytes(int H, int I, int T, bool backward) { return ffn_layout(H, I, T, backward).total; }
+size_t ffn_workspace_bytes(int H, int I, int T, bool backward) { return ffn_layout(I, T, backward).total; }
 
 cudaError_t launch_ffn_forward(const FfnCall& c, int num_sms, cudaStream_t s) {
   char* ws = static_cast<char*>(c.ws);
-  const FfnLayout l = ffn_layout(c.H, c.I, c.T, false);
+  const FfnLayout l = ffn_layout(c.I, c.T, false);
   void* h = ws + l.h;
   GemmArgs a{};
   a.bf16 = c.type == MOE_BF16;
@@ -886,18 +948,21 @@ cudaError_t launch_ffn_forward(const FfnCall& c, int num_sms, cudaStream_t s) {
   a.reset = 1;
   a.p[0] = problem(c.T, 2 * c.I, c.H, 0, 0, h);
   a.p[0].ld = c.I;
+  const bool few = c.T <= kRest;
+  a.p[0].rest = few;
   const Operands gu{c.x, c.T, c.H, c.w_gate_up, 2 * c.I, c.H};
   cudaError_t e = launch_products<EPI_GATED>(a, &gu, num_sms, s);
   if (e != cudaSuccess) return e;
   a.reset = 0;
   a.p[0] = problem(c.T, c.H, c.I, 0, 0, c.y);
-  const Operands dn{h, c.T, c.I, c.w_down, c.H, c.I};
+  a.p[0].fold = few;
+  const Operands dn{h, few ? kRest + c.T : c.T, c.I, c.w_down, c.H, c.I};
   return launch_products<EPI_STORE>(a, &dn, num_sms, s);
 }
 
 cudaError_t launch_ffn_backward(const FfnCall& c, int num_sms, cudaStream_t s) {
   char* ws = static_cast<char*>(c.ws);
-  const FfnLayout l = ffn_layout(c.H, c.I, c.T, true);
+  const FfnLayout l = ffn_layout(c.I, c.T, true);
   void* h = ws + l.h;
   void* dgu = ws + l.dgu;
   GradArgs g{};
@@ -908,11 +973,14 @@ cudaError_t launch_ffn_backward(const FfnCall& c, int num_sms, cudaStream_t s) {
   g.h = c.dw_down ? static_cast<uint16_t*>(h) : nullptr;
   g.dgu = static_cast<uint16_t*>(dgu);
   g.status = reinterpret_cast<int*>(ws + l.status);
+  const bool few = c.T <= kRest;
+  g.rest = few;
+  const int rows = few ? 2 * kRest : c.T;          // of h and dgu
   // a step of both reductions: 800 cycles on the wide tile, 600 on the narrow
   // one, whose reductions can be split
   const double wide = tile_time(ceil_div(c.T, 256) * ceil_div(c.I, 128), g.kblocks, 2, 1, 800, num_sms);
   const double narrow = tile_time(ceil_div(c.T, 128) * ceil_div(c.I, 64), g.kblocks, 1, 4, 600, num_sms);
-  cudaError_t e = wide <= narrow ? launch_grad<2, 128>(g, c, num_sms, s) : launch_grad<1, 64>(g, c, num_sms, s);
+  cudaError_t e = !few && wide <= narrow ? launch_grad<2, 128>(g, c, num_sms, s) : launch_grad<1, 64>(g, c, num_sms, s);
   if (e != cudaSuccess) return e;
 
   GemmArgs a{};
@@ -922,16 +990,28 @@ cudaError_t launch_ffn_backward(const FfnCall& c, int num_sms, cudaStream_t s) {
   Problem p[3];
   int n = 0;
   if (c.dx) {
-    op[n] = {dgu, c.T, 2 * c.I, c.w_gate_up, 2 * c.I, c.H};
-    p[n++] = problem(c.T, c.H, 2 * c.I, 0, 1, c.dx);
+    op[n] = {dgu, rows, 2 * c.I, c.w_gate_up, 2 * c.I, c.H};
+    p[n] = problem(c.T, c.H, 2 * c.I, 0, 1, c.dx);
+    p[n++].fold = few;
   }
+  if (few && n > 0) {       // a launch of its own: its reduction is deep and split, the others' is 128
+    a.n = 1;
+    a.p[0] = p[0];
+    e = launch_products<EPI_STORE>(a, op, num_sms, s);
+    if (e != cudaSuccess) return e;
+    n = 0;
+  }
+  // few tokens: the reduction runs over the rounded rows and their rests, 64
+  // each, with the other operand's 64 rows taken again
   if (c.dw_gate_up) {
-    op[n] = {dgu, c.T, 2 * c.I, c.x, c.T, c.H};
-    p[n++] = problem(2 * c.I, c.H, c.T, 1, 1, c.dw_gate_up);
+    op[n] = {dgu, rows, 2 * c.I, c.x, c.T, c.H};
+    p[n] = problem(2 * c.I, c.H, few ? rows : c.T, 1, 1, c.dw_gate_up);
+    p[n++].b_step = few ? 0 : BK;
   }
   if (c.dw_down) {
-    op[n] = {c.dy, c.T, c.H, h, c.T, c.I};
-    p[n++] = problem(c.H, c.I, c.T, 1, 1, c.dw_down);
+    op[n] = {c.dy, c.T, c.H, h, rows, c.I};
+    p[n] = problem(c.H, c.I, few ? rows : c.T, 1, 1, c.dw_down);
+    p[n++].a_step = few ? 0 : BK;
   }
   if (n == 0) return cudaSuccess;
   // the deepest products first: the last tiles to finish are short ones

@@ -114,6 +114,8 @@ SHAPES = [
     (512, 2048, 4096), (1111, 1000, 3144), (2049, 2056, 1032),
     # a tile's reduction split over a cluster: by 4 and 2 on narrow tiles, over two pairs on wide ones, uneven parts
     (5, 1032, 520), (100, 2048, 256), (130, 776, 1096), (777, 2056, 5000), (500, 1024, 4104),
+    # few tokens (the rest of h's and dgu's rounding is kept) on either tile
+    (64, 1024, 4096), (33, 4096, 8000), (16, 2048, 8192),
 ]
 
 
@@ -150,7 +152,7 @@ def torch_ref(x, wgu, wd, dy=None):
                         dy.abs().T @ (h.abs() * hs + hl * 2.0 ** -20)))
 
 
-def check(got, ref, spread, t, terms, what):
+def check(got, ref, spread, t, terms, what, tokens):
     """Element by element: the operand's rounding (half a step of every term), the
     fp32 sum (2^-20 of the terms' magnitudes: the tensor core's own additions,
     `terms` / 16 of them at 2^-24) and the output's half step; a value below the
@@ -164,6 +166,9 @@ def check(got, ref, spread, t, terms, what):
     assert bool((err <= tol).all()), (what, float((err / tol).max()))
     if ref.numel() >= 4096:
         assert float(err.norm() / ref.norm()) <= hs, what
+        # up to 64 tokens only the output is rounded: half a step / sqrt(3) at most
+        if tokens <= 64:
+            assert float(err.norm() / ref.norm()) <= 0.6 * hs, what
 
 
 @gpu
@@ -185,7 +190,7 @@ def test_forward(T, H, I, dtype):
     hl = (g[:, 0::2] * 1.1 * gu[:, 1::2].abs() + gu[:, 0::2].abs() * g[:, 1::2]) @ wd.double().abs().T
     hs = torch.finfo(t).eps / 2
     tiny = torch.finfo(t).tiny * torch.finfo(t).eps * wd.double().abs().sum(1)
-    check(y, ref, mag * (hs + 2.0 ** -20) + hl * 2.0 ** -20 + tiny, t, I, "y")
+    check(y, ref, mag * (hs + 2.0 ** -20) + hl * 2.0 ** -20 + tiny, t, I, "y", T)
 
 
 @gpu
@@ -206,7 +211,7 @@ def test_backward(T, H, I, dtype):
     tiny = (wgu.double().abs().sum(0)[None], x.double().abs().sum(0)[None], dy.double().abs().sum(0)[:, None])
     for got, ref, sp, tn, n, what in zip(out, refs, spread(hs + 2.0 ** -20), tiny, (2 * I, T, T),
                                          ("dx", "dw_gate_up", "dw_down")):
-        check(got, ref, sp + tn * least, t, n, what)
+        check(got, ref, sp + tn * least, t, n, what, T)
 
 
 @gpu
