@@ -28,7 +28,15 @@
 // copies in the 128-byte swizzle, either contiguous along the reduction or
 // along the row (transposed operands are never copied: the instruction reads
 // both).  Roles: epilogue warps, one producer, one issuer; two accumulators,
-// so that a tile's epilogue runs under the next one's products.
+// so that a tile's epilogue runs under the next one's products.  Where there
+// are few tiles a cluster splits one tile's reduction and joins the partial
+// sums over distributed shared memory.
+//
+// Measured on one B200, 8192 tokens x 2048 x 8192 bf16: forward 540-550 us (1500
+// TFLOP/s, tensor pipe 97% and 94% active, the clock at 1.5 GHz under the power
+// cap), backward 1525-1565 us (16 T H I: 1420 TFLOP/s; 77% in the first launch,
+// whose dh products have half the columns, 98% in the second).  One token x
+// 2048 x 768: 14.6 us, of which the launches' own start and the joins are most.
 #include "dense_internal.cuh"
 #include "tensor_core.cuh"
 
