@@ -607,6 +607,7 @@ Plan plan_linear(int N, int nb, int T, int num_sms) {
         p.groups = min(gmax, (tiles + sms - 1) / sms);
         p.ctas = min((tiles + p.groups - 1) / p.groups, sms);
         p.smem = linear_smem(ring, CB, p.cpr, p.tt, groups_of_8(p.tt), p.groups, KG, C);
+        if (groups_of_8(p.tt) == 8 && CB == 8) continue;      // 64 tokens' sums and 8 blocks' scales spill
         const int NT = groups_of_8(p.tt), per = (tiles + p.ctas - 1) / p.ctas, waves = (p.ny * p.ctas + at_once - 1) / at_once;
         const int rounds = (per + p.groups - 1) / p.groups, stages = (p.cpr + KG - 1) / KG;
         const double block = 6 + 13.5 * NT, stage = 250 + CB * (25 + 15 * NT);
@@ -681,7 +682,6 @@ cudaError_t launch_linear(const LinearCall& c, int num_sms, cudaStream_t s) {
     case 1 * 16 + 8: return launch_fmt<1, 8>(fmt, a, grid, p.smem, s);
     case 2 * 16 + 8: return launch_fmt<2, 8>(fmt, a, grid, p.smem, s);
     case 4 * 16 + 8: return launch_fmt<4, 8>(fmt, a, grid, p.smem, s);
-    case 8 * 16 + 8: return launch_fmt<8, 8>(fmt, a, grid, p.smem, s);
     case 1 * 16 + 4: return launch_fmt<1, 4>(fmt, a, grid, p.smem, s);
     case 2 * 16 + 4: return launch_fmt<2, 4>(fmt, a, grid, p.smem, s);
     case 4 * 16 + 4: return launch_fmt<4, 4>(fmt, a, grid, p.smem, s);
