@@ -26,7 +26,7 @@
 // largest one, off by at most 2^-38 of it below (fp32 sums lose more).  A row
 // with an infinity or a NaN gives NaN in all its outputs.
 //
-// Each warp streams its own stages of 16 rows x 128 or 256 columns through a
+// Each warp streams its own stages of 16 rows x 128 to 512 columns through a
 // private ring of asynchronous copies (no block-wide barrier in the stream);
 // the warps of a group split the columns of a row tile, so that even 2048 x
 // 2048 spreads over 128 SMs, and join their fp32 sums through shared memory in
@@ -37,10 +37,10 @@
 // memory while the next tile's stages are multiplied.
 //
 // Measured on one B200 (weights from HBM, rotating): 4 tokens x 100003 x 2048
-// 29.2 us (4.0 TB/s of 6.5; the stream without the products 20.2), 1 x 2048 x
-// 2048 4.1 us, 1 x 40000 x 4096 25 us (3.6 TB/s).  What bounds the large ones is
-// issue: 48 warp instructions a block of 16 x 32 (31 of them decode, products
-// and folds), 62% of the issue slots; the mask and shift pipe and the tensor
+// 27.4 us (4.3 TB/s of 6.5; the stream without the products 20.2), 1 x 2048 x
+// 2048 4.1 us, 1 x 40000 x 4096 24 us (3.8 TB/s).  What bounds the large ones is
+// issue: 31 warp instructions a block of 16 x 32 for decode, products and folds
+// and 8 to 17 for the stage around them, 62% of the issue slots; the mask and shift pipe and the tensor
 // instruction do not overlap (13 cycles a block in isolation, 4.4 without the
 // decode).  Tried: tensor copies for the codes (+10%), 24 or 32 warps (no
 // change), codes as subnormals (27.5 us, and the rounding above).
@@ -64,14 +64,16 @@ struct Format {
   static constexpr int SB = FMT == F_E32 ? 1 : 2;            // bytes of a scale
 };
 // A stage: 16 rows x CB blocks of 32 columns, codes then scales (up to CB fp16
-// a row), in a ring of ST slots per warp.  8 blocks halve the per-stage work;
-// 4 leave room for more activations.
+// a row), in a ring of ST slots per warp.  A stage costs about 130
+// instructions besides its blocks: 16 blocks for up to 8 tokens (4 x 100003 x
+// 2048: 27.4 us, 29.2 with 8), 8 for up to 32, 4 where the activations need the
+// room or a row is short.
 template <int CB>
 struct Stage {
   static constexpr int ROW = CB * 16;
   static constexpr int CODES = 16 * ROW;
   static constexpr int BYTES = CODES + 32 * CB;
-  static constexpr int ST = CB == 8 ? 3 : 4;
+  static constexpr int ST = CB == 16 ? 2 : CB == 8 ? 3 : 4;
   static constexpr int RING = kWarps * ST * BYTES;
 };
 
@@ -117,9 +119,8 @@ template <int FMT, int CB>
 __device__ __forceinline__ void stage_scales(const unsigned char* sc, int row, float (&s)[CB]) {
   if (Format<FMT>::G128) {
     const __half* p = reinterpret_cast<const __half*>(sc) + row * (CB / 4);
-    const float a = __half2float(p[0]), b = CB == 8 ? __half2float(p[1]) : a;
 #pragma unroll
-    for (int i = 0; i < CB; ++i) s[i] = i < 4 ? a : b;
+    for (int i = 0; i < CB; i += 4) s[i] = s[i + 1] = s[i + 2] = s[i + 3] = __half2float(p[i / 4]);
   } else {
     uint32_t w[CB / 2];
     if (FMT == F_E32) {
@@ -130,9 +131,12 @@ __device__ __forceinline__ void stage_scales(const unsigned char* sc, int row, f
             "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
             : "=r"(w[2 * i]), "=r"(w[2 * i + 1]) : "r"(v));
       }
-    } else if (CB == 8) {
-      const uint4 v = *reinterpret_cast<const uint4*>(sc + row * 16);
-      w[0] = v.x; w[1] = v.y; w[CB / 2 - 2] = v.z; w[CB / 2 - 1] = v.w;
+    } else if (CB >= 8) {
+#pragma unroll
+      for (int i = 0; i < CB / 8; ++i) {
+        const uint4 v = *reinterpret_cast<const uint4*>(sc + row * (2 * CB) + 16 * i);
+        w[4 * i] = v.x; w[4 * i + 1] = v.y; w[(4 * i + 2) % (CB / 2)] = v.z; w[(4 * i + 3) % (CB / 2)] = v.w;
+      }
     } else {
       const uint2 v = *reinterpret_cast<const uint2*>(sc + row * 8);
       w[0] = v.x; w[1] = v.y;
@@ -200,7 +204,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const LinearArgs a)
   const int total = my_tiles * my_chunks;
 
   // ------------------------------------------------------ weight stream
-  // This lane copies CB / 4 x 2 16-byte pieces of a stage's codes: piece
+  // This lane copies CB / 2 16-byte pieces of a stage's codes: piece
   // `ch` of the rows r0 + i * RS, swizzled so that the words of eight rows
   // fall into different banks.
   unsigned char* ring = lsm + warp * (S::ST * S::BYTES);
@@ -213,6 +217,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const LinearArgs a)
   // alignment, or one fp16 per stage) pass through registers: loaded with
   // their stage's codes, stored to its slot when the next stage is issued
   constexpr bool kMayCopy = SPC * F::SB >= 4;
+  constexpr bool kTwo = SPC * F::SB == 32;                // 32 bytes of scales a row: two copies
   const bool direct = kMayCopy && a.spr % SPC == 0;
   constexpr int PEND = (16 * SPC + 31) / 32;
   uint16_t pend[PEND];
@@ -239,7 +244,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const LinearArgs a)
   for (int i = 0; i < CB / 2; ++i) {
     const int r = r0 + i * RS;
     row_off[i] = i * RS * row_bytes;
-    dst_off[i] = r * S::ROW + ((ch ^ (CB == 8 ? r & 7 : (r >> 1) & 3)) << 4);
+    dst_off[i] = r * S::ROW + ((ch ^ (CB >= 8 ? r & 7 : (r >> 1) & 3)) << 4);
   }
   auto enter_tile = [&]() {
     it_chunk = c_lo + kw;
@@ -249,7 +254,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const LinearArgs a)
     }
     src = a.codes + size_t(it_tile * 16 + r0) * row_bytes + size_t(it_chunk) * S::ROW + ch * 16;
     ssrc = static_cast<const uint8_t*>(a.scales) +
-           (size_t(min(it_tile * 16 + (lane & 15), a.N - 1)) * a.spr + size_t(it_chunk) * SPC) * F::SB;
+           (size_t(min(it_tile * 16 + (kTwo ? lane >> 1 : lane & 15), a.N - 1)) * a.spr + size_t(it_chunk) * SPC) * F::SB +
+           (kTwo ? (lane & 1) * 16 : 0);
   };
   if (left > 0) enter_tile();
   auto issue = [&]() {
@@ -261,9 +267,9 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const LinearArgs a)
         for (int i = 0; i < CB / 2; ++i) cp_async16(dst + dst_off[i], src + row_off[i]);
       }
       if (direct) {
-        if (lane < 16) {
-          constexpr int B = kMayCopy ? SPC * F::SB : 4;
-          if (B == 16) cp_async16(dst + S::CODES + lane * 16, ssrc);
+        constexpr int B = kTwo ? 16 : kMayCopy ? SPC * F::SB : 4;
+        if (kTwo || lane < 16) {
+          if (B == 16) cp_async16(dst + S::CODES + lane * B, ssrc);
           else cp_async_small<B == 16 ? 8 : B>(dst + S::CODES + lane * B, ssrc);
         }
       } else {
@@ -376,7 +382,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const LinearArgs a)
   const unsigned char* xrow[NT];
 #pragma unroll
   for (int j = 0; j < NT; ++j) xrow[j] = sx + min(8 * j + g, nt - 1) * xpitch + t * 16;
-  const uint32_t lane_code = uint32_t(g * S::ROW + ((CB == 8 ? g : (g >> 1) & 3) << 4) + t * 4);
+  const uint32_t lane_code = uint32_t(g * S::ROW + ((CB >= 8 ? g : (g >> 1) & 3) << 4) + t * 4);
   float acc[NT][4];
 #pragma unroll
   for (int j = 0; j < NT; ++j)
@@ -582,13 +588,13 @@ Plan plan_linear(int N, int nb, int T, int num_sms) {
   const int tiles = (N + 15) / 16;
   for (int C = 1; C <= 8; C *= 2) {
     const int at_once = clusters_at_once(C, num_sms);
-    for (int CB = 8; CB >= 4; CB -= 4) {
+    for (int CB = 16; CB >= 4; CB /= 2) {
       Plan p{};
       p.C = C; p.CB = CB;
       p.chunks = (nb + CB - 1) / CB;
       p.cpr = (p.chunks + C - 1) / C;
       if (C > 1 && (C - 1) * p.cpr >= p.chunks) continue;      // a rank without columns
-      const int ring = CB == 8 ? Stage<8>::RING : Stage<4>::RING;
+      const int ring = CB == 16 ? Stage<16>::RING : CB == 8 ? Stage<8>::RING : Stage<4>::RING;
       for (int KG = 1; KG <= kWarps; KG *= 2) {
         if (KG > p.cpr && KG > 1) break;
         p.KG = KG;
@@ -607,11 +613,12 @@ Plan plan_linear(int N, int nb, int T, int num_sms) {
         p.groups = min(gmax, (tiles + sms - 1) / sms);
         p.ctas = min((tiles + p.groups - 1) / p.groups, sms);
         p.smem = linear_smem(ring, CB, p.cpr, p.tt, groups_of_8(p.tt), p.groups, KG, C);
-        if (groups_of_8(p.tt) == 8 && CB == 8) continue;      // 64 tokens' sums and 8 blocks' scales spill
+        if ((groups_of_8(p.tt) == 8 && CB == 8) || (groups_of_8(p.tt) > 1 && CB == 16)) continue;   // more sums and scales spill
         const int NT = groups_of_8(p.tt), per = (tiles + p.ctas - 1) / p.ctas, waves = (p.ny * p.ctas + at_once - 1) / at_once;
         const int rounds = (per + p.groups - 1) / p.groups, stages = (p.cpr + KG - 1) / KG;
-        const double block = 6 + 13.5 * NT, stage = 250 + CB * (25 + 15 * NT);
-        const double thr = per * (double(p.cpr) * CB * block + 60 + KG * (10 + 4 * NT));
+        // a stage: of the SM's issue slots, and for a warp alone
+        const double busy = CB * (6 + 13.5 * NT) * (CB == 16 ? 0.94 : 1), stage = 250 + CB * (25 + 15 * NT);
+        const double thr = per * (p.cpr * busy + 60 + KG * (10 + 4 * NT));
         const double lat = rounds * (stages * stage + 200 + (C > 1 ? 100 : 0));
         p.cost = waves * (5000 + p.tt * double(p.cpr) * CB * 32 * 0.1 + (C > 1 ? 2500 : 0) + thr + 0.5 * lat);
         if (best.cost < 0 || p.cost < best.cost) best = p;
@@ -678,13 +685,14 @@ cudaError_t launch_linear(const LinearCall& c, int num_sms, cudaStream_t s) {
   if (p.cost < 0) return cudaErrorInvalidConfiguration;
   a.chunks = p.chunks; a.C = p.C; a.cpr = p.cpr; a.KG = p.KG; a.groups = p.groups; a.ny = p.ny; a.tt = p.tt;
   const int grid = p.C * p.ny * p.ctas;
-  switch (groups_of_8(p.tt) * 16 + p.CB) {
-    case 1 * 16 + 8: return launch_fmt<1, 8>(fmt, a, grid, p.smem, s);
-    case 2 * 16 + 8: return launch_fmt<2, 8>(fmt, a, grid, p.smem, s);
-    case 4 * 16 + 8: return launch_fmt<4, 8>(fmt, a, grid, p.smem, s);
-    case 1 * 16 + 4: return launch_fmt<1, 4>(fmt, a, grid, p.smem, s);
-    case 2 * 16 + 4: return launch_fmt<2, 4>(fmt, a, grid, p.smem, s);
-    case 4 * 16 + 4: return launch_fmt<4, 4>(fmt, a, grid, p.smem, s);
+  switch (groups_of_8(p.tt) * 32 + p.CB) {
+    case 1 * 32 + 16: return launch_fmt<1, 16>(fmt, a, grid, p.smem, s);
+    case 1 * 32 + 8: return launch_fmt<1, 8>(fmt, a, grid, p.smem, s);
+    case 2 * 32 + 8: return launch_fmt<2, 8>(fmt, a, grid, p.smem, s);
+    case 4 * 32 + 8: return launch_fmt<4, 8>(fmt, a, grid, p.smem, s);
+    case 1 * 32 + 4: return launch_fmt<1, 4>(fmt, a, grid, p.smem, s);
+    case 2 * 32 + 4: return launch_fmt<2, 4>(fmt, a, grid, p.smem, s);
+    case 4 * 32 + 4: return launch_fmt<4, 4>(fmt, a, grid, p.smem, s);
     default: return launch_fmt<8, 4>(fmt, a, grid, p.smem, s);
   }
 }

@@ -139,6 +139,7 @@ CASES = [
     # T, rows, cols: every token group size, ragged rows, one block, columns off the stage and the copy width
     (1, 1, 32), (1, 16, 64), (2, 17, 96), (3, 15, 128), (5, 33, 160), (8, 256, 256), (1, 2048, 2048), (7, 100, 2080),
     (9, 48, 1056), (16, 130, 4096), (17, 64, 4128), (32, 31, 2048), (33, 50, 512), (64, 77, 8192), (100, 40, 1024), (48, 300, 544), (10, 700, 4096), (16, 150000, 128), (12, 40, 32), (1000, 64, 512), (64, 20481, 1056),
+    (3, 40001, 1056), (8, 30000, 2048), (1, 50000, 512),
     (1, 3000, 768), (4, 40, 32768),
 ]
 
@@ -283,15 +284,18 @@ def test_repeats_and_stays_inside_its_output(T, rows, cols, out):
 
 
 @gpu
-def test_streams_and_graphs():
+@pytest.mark.parametrize("T,rows,cols,out", [(4, 512, 1024, "bfloat16"), (16, 2050, 8192, "bfloat16"),
+                                             (16, 2050, 8192, "float32"), (64, 8192, 4096, "bfloat16")])
+def test_streams_and_graphs(T, rows, cols, out):
     """Two streams at once, and a captured call replayed on new inputs."""
     import torch
-    codes, scales, rs, _, _ = matrix(512, 1024, seed=12)
+    yt = getattr(torch, out)
+    codes, scales, rs, _, _ = matrix(rows, cols, seed=12)
     cfg = q.linear_config_of()
-    xs = [tokens(4, 1024, torch.bfloat16, seed=s) for s in range(2)]
+    xs = [tokens(T, cols, torch.bfloat16, seed=s) for s in range(2)]
     want = []
     for x in xs:
-        y = torch.empty(4, 512, dtype=torch.bfloat16, device="cuda")
+        y = torch.empty(T, rows, dtype=yt, device="cuda")
         q.moe_linear_forward(cfg, codes, scales, x, y)
         want.append(y)
     torch.cuda.synchronize()
@@ -305,19 +309,21 @@ def test_streams_and_graphs():
     x, y = xs[0].clone(), torch.empty_like(want[0])
     g = torch.cuda.CUDAGraph()
     with torch.cuda.graph(g):
-        q.moe_linear_forward(cfg, codes, scales, x, y)
+        for _ in range(3):                                   # each waits for the one before it
+            q.moe_linear_forward(cfg, codes, scales, x, y)
     for k in (1, 0):
         x.copy_(xs[k])
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(y, want[k])
+    assert q.moe_linear_device_status() == 0
 
 
 @gpu
-def test_packed_block_serves():
+@pytest.mark.parametrize("T,H,I", [(5, 512, 384), (48, 2048, 4096)])
+def test_packed_block_serves(T, H, I):
     """Gate/up then down, as a dense block is served: against the definition in 64 bits."""
     import torch
-    T, H, I = 5, 512, 384
     cgu, sgu, _, wgu, _ = matrix(2 * I, H, seed=13)
     cd, sd, _, wd, _ = matrix(H, I, seed=14)
     cfg = q.linear_config_of()
@@ -332,6 +338,12 @@ def test_packed_block_serves():
     z = xd @ wgu.T
     hid = z[:, 0::2] / (1 + np.exp(-z[:, 0::2])) * z[:, 1::2]
     ref = hid @ wd.T
-    # h rounds to fp16 (2^-11 of each element, and 2^-25 below its smallest step); the rest is fp32
-    tol = (np.abs(hid) * 2.0 ** -11 + 2.0 ** -25) @ np.abs(wd).T * 1.01 + np.abs(ref) * 2.0 ** -18
+    # h rounds to fp16 (2^-11 of each element, and 2^-25 below its smallest step), with more than 8 tokens after its
+    # weights did (2^-11 of every term, through both factors); the rest is fp32
+    dh = np.abs(hid) * 2.0 ** -11 + 2.0 ** -25
+    if T > 8:
+        m = np.abs(xd) @ np.abs(wgu).T * 2.0 ** -11
+        g, u = z[:, 0::2], z[:, 1::2]
+        dh = dh + (np.abs(u) + m[:, 1::2]) * 1.1 * m[:, 0::2] + np.abs(g) * m[:, 1::2]
+    tol = dh @ np.abs(wd).T * 1.01 + np.abs(ref) * 2.0 ** -18
     assert (np.abs(y.double().cpu().numpy() - ref) <= tol).all()
