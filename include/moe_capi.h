@@ -283,9 +283,12 @@ int moe_linear_device_status(int32_t* code_out);
  *   w_down    [hidden][inter],  x, y [T][hidden]
  * All arrays dense, row-major, 16-byte aligned; y overlaps nothing.  hidden and
  * inter multiples of 8, at most 65536; any T >= 0 up to 2^22.  g, u and every
- * sum are fp32; h is rounded to 16 bits between the two products and y once.
+ * sum are fp32; h is rounded to 16 bits between the two products and y once (up
+ * to 64 tokens: h keeps what that rounding leaves, only y is rounded).
  * The workspace (256-byte aligned, moe_ffn_workspace_bytes) holds h; its first
- * words are the device check that moe_device_status reads. */
+ * words are the device check that moe_device_status reads.  This call and the
+ * next read weights before they wait for a kernel ahead of them that lets its
+ * dependents launch early; none in this library writes weights. */
 int moe_ffn_forward(int32_t hidden, int32_t inter, int32_t type, const void* w_gate_up, const void* w_down,
                     const void* x, int32_t T, void* y, void* workspace, size_t ws_bytes, void* stream);
 
@@ -296,7 +299,8 @@ int moe_ffn_forward(int32_t hidden, int32_t inter, int32_t type, const void* w_g
  * from x, dy and the weights alone: the projections are computed again, so the
  * forward call keeps nothing.  An output that is NULL is not computed.  Outputs
  * are overwritten (no accumulation) and overlap nothing.  dg, du and h are
- * rounded to 16 bits between the products, everything else is fp32.  T == 0
+ * rounded to 16 bits between the products (up to 64 tokens they keep what that
+ * leaves), everything else is fp32.  T == 0
  * clears the weight gradients. */
 int moe_ffn_backward(int32_t hidden, int32_t inter, int32_t type, const void* w_gate_up, const void* w_down,
                      const void* x, const void* dy, int32_t T, void* dx, void* dw_gate_up, void* dw_down,

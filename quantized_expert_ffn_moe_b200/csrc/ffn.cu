@@ -36,7 +36,7 @@
 // TFLOP/s, tensor pipe 97% and 94% active, the clock at 1.5 GHz under the power
 // cap), backward 1525-1565 us (16 T H I: 1420 TFLOP/s; 77% in the first launch,
 // whose dh products have half the columns, 98% in the second).  One token x
-// 2048 x 768: 14.6 us, of which the launches' own start and the joins are most.
+// 2048 x 768: 14.3 us, of which the launches' own start and the joins are most.
 #include "dense_internal.cuh"
 #include "tensor_core.cuh"
 
@@ -70,6 +70,7 @@ struct Problem {
   int a_step, b_step;    // the operands' coordinate along the reduction: BK a step, 0 to take the same 64 again
   int rest;              // EPI_GATED: what the rounding of a row leaves goes kRest rows further down
   int fold;              // rows kRest further down are added to a row (one tile per CTA)
+  int weights;           // B is weights: its first stages are asked for before the previous kernel has ended
   void* out;
   int ld;
 };
@@ -219,8 +220,10 @@ template <int CG, bool AMN, bool BMN, int BROWS, int STAGE, int STAGES>
 __device__ __forceinline__ bool load_steps(uint32_t ring, uint64_t* full, uint64_t* empty, uint32_t full_leader, int rank,
                                            Cursor<STAGES>& c, const CUtensorMap* ma, const CUtensorMap* mb, int row_a,
                                            int row_b, int a_step, int b_step, int kb0, int steps,
-                                           const volatile int* abort_flag) {
-  for (int kb = kb0; kb < kb0 + steps; ++kb) {
+                                           int pre, const volatile int* abort_flag) {
+  for (int kb = kb0; kb < kb0 + pre; ++kb, c.next())          // preload_b has asked for the other operand
+    load_operand<CG, AMN, 128>(ring + uint32_t(c.s) * STAGE, ma, row_a, kb * a_step, full_leader + uint32_t(c.s) * 8);
+  for (int kb = kb0 + pre; kb < kb0 + steps; ++kb) {
     if (!mbar_wait(&empty[c.s], c.parity ^ 1u, abort_flag)) return false;
     if (rank == 0) mbar_arrive_expect_tx(&full[c.s], CG * (kAStage + BROWS * 128));
     const uint32_t st = ring + uint32_t(c.s) * STAGE, bar = full_leader + uint32_t(c.s) * 8;
@@ -229,6 +232,18 @@ __device__ __forceinline__ bool load_steps(uint32_t ring, uint64_t* full, uint64
     c.next();
   }
   return true;
+}
+// B of the ring's first stages, for weights: their way from memory runs under
+// the end of the previous kernel of the stream.  The number of stages.
+template <int CG, bool BMN, int BROWS, int STAGE, int STAGES>
+__device__ __forceinline__ int preload_b(uint32_t ring, uint64_t* full, uint32_t full_leader, int rank, const CUtensorMap* mb,
+                                         int row_b, int b_step, int kb0, int steps) {
+  const int pre = min(steps, STAGES);
+  for (int s = 0; s < pre; ++s) {
+    if (rank == 0) mbar_arrive_expect_tx(&full[s], CG * (kAStage + BROWS * 128));
+    load_operand<CG, BMN, BROWS>(ring + uint32_t(s) * STAGE + kAStage, mb, row_b, (kb0 + s) * b_step, full_leader + uint32_t(s) * 8);
+  }
+  return pre;
 }
 // The products of `steps` stages into the accumulator at d, by one warp: one
 // lane issues.  A stage is four instructions of 16 deep.
@@ -380,10 +395,6 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ffn_gemm_kernel(const __grid_
   else cluster_sync();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  pdl_wait();
-  pdl_launch_dependents();
-  if (a.reset && blockIdx.x == 0 && threadIdx.x == 0) { a.status[0] = 0; a.status[1] = 0; }
-
   const int unit = int(blockIdx.x) / (CG * split), units = int(gridDim.x) / (CG * split);
   // Round by round, every other one backwards: the list is sorted by depth, so
   // who had a deep tile gets a shallow one next.
@@ -395,10 +406,30 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ffn_gemm_kernel(const __grid_
     return i;
   };
 
+  const uint32_t leader = CG == 1 ? smem_u32(full) : in_leader(full);
+  int pre = 0;
+  if (warp == kEpiWarps && lane == 0 && unit < a.ntiles) {
+    int m, n;
+    const int i = find(turn(0), &m, &n);
+    const Problem& p = a.p[i];
+    if (p.weights) {
+      const Part kp = part_of(p.kblocks, split, srank);
+      const int row_b = n * BN + rank * T::BROWS;
+      pre = p.b_mn ? preload_b<CG, true, T::BROWS, T::STAGE, T::STAGES>(smem_u32(base), full, leader, rank, &maps.b[i], row_b,
+                                                                      p.b_step, kp.first, kp.steps)
+                   : preload_b<CG, false, T::BROWS, T::STAGE, T::STAGES>(smem_u32(base), full, leader, rank, &maps.b[i], row_b,
+                                                                       p.b_step, kp.first, kp.steps);
+    }
+  }
+  __syncwarp();
+  pdl_wait();
+  pdl_launch_dependents();
+  if (a.reset && blockIdx.x == 0 && threadIdx.x == 0) { a.status[0] = 0; a.status[1] = 0; }
+
   if (warp == kEpiWarps && lane == 0) {
     // ------------------------------------------------------- producer
     Cursor<T::STAGES> c;
-    const uint32_t ring = smem_u32(base), leader = CG == 1 ? smem_u32(full) : in_leader(full);
+    const uint32_t ring = smem_u32(base);
     bool ok = true;
     for (int tc = 0, t; (t = turn(tc)) < a.ntiles && ok; ++tc) {
       int m, n;
@@ -409,7 +440,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ffn_gemm_kernel(const __grid_
       auto run = [&](auto amn, auto bmn) {
         return load_steps<CG, amn.value, bmn.value, T::BROWS, T::STAGE, T::STAGES>(
             ring, full, empty, leader, rank, c, &maps.a[i], &maps.b[i], row_a, row_b, p.a_step, p.b_step, kp.first, kp.steps,
-            abort_flag);
+            tc == 0 ? pre : 0, abort_flag);
       };
       ok = p.a_mn ? run(Yes(), Yes()) : p.b_mn ? run(No(), Yes()) : run(No(), No());
     }
@@ -617,10 +648,6 @@ __global__ void __launch_bounds__(kGradThreads, 1) ffn_grad_kernel(const __grid_
   else cluster_sync();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  pdl_wait();
-  pdl_launch_dependents();
-  if (a.reset && blockIdx.x == 0 && threadIdx.x == 0) { a.status[0] = 0; a.status[1] = 0; }
-
   const int unit = int(blockIdx.x) / (CG * split), units = int(gridDim.x) / (CG * split);
   const int ntiles = a.tiles_m * a.tiles_n;
   const int rows = a.rest ? kRest : a.T;          // of h and dgu that are written (and as many of the rest)
@@ -628,9 +655,22 @@ __global__ void __launch_bounds__(kGradThreads, 1) ffn_grad_kernel(const __grid_
   shape.tiles_m = a.tiles_m;
   shape.tiles_n = a.tiles_n;
 
+  const uint32_t leader = CG == 1 ? smem_u32(full) : in_leader(full);
+  int pre = 0;
+  if (warp == kGradEpi && lane == 0 && unit < ntiles) {
+    int m, n;
+    tile_of(shape, unit, &m, &n);
+    pre = preload_b<CG, false, T::BROWS, T::STAGE, T::STAGES>(smem_u32(base), full, leader, rank, &tm_wgu,
+                                                            n * 2 * NI + rank * T::BROWS, BK, kp.first, kp.steps);
+  }
+  __syncwarp();
+  pdl_wait();
+  pdl_launch_dependents();
+  if (a.reset && blockIdx.x == 0 && threadIdx.x == 0) { a.status[0] = 0; a.status[1] = 0; }
+
   if (warp == kGradEpi && lane == 0) {
     Cursor<T::STAGES> c;
-    const uint32_t ring = smem_u32(base), leader = CG == 1 ? smem_u32(full) : in_leader(full);
+    const uint32_t ring = smem_u32(base);
     bool ok = true;
     for (int t = unit; t < ntiles && ok; t += units) {
       int m, n;
@@ -638,10 +678,10 @@ __global__ void __launch_bounds__(kGradThreads, 1) ffn_grad_kernel(const __grid_
       const int row_a = m * T::BM + rank * 128;
       ok = load_steps<CG, false, false, T::BROWS, T::STAGE, T::STAGES>(ring, full, empty, leader, rank, c, &tm_x, &tm_wgu,
                                                                       row_a, n * 2 * NI + rank * T::BROWS, BK, BK, kp.first,
-                                                                      kp.steps, abort_flag) &&
+                                                                      kp.steps, t == unit ? pre : 0, abort_flag) &&
            load_steps<CG, false, true, DROWS, T::STAGE, T::STAGES>(ring, full, empty, leader, rank, c, &tm_dy, &tm_wd,
                                                                   row_a, n * NI + rank * DROWS, BK, BK, kp.first, kp.steps,
-                                                                  abort_flag);
+                                                                  0, abort_flag);
     }
     if (!ok) { *abort_flag = 1; report_error(a.status, MOE_ERR_TIMEOUT, 60); }
     if (ok ? !settled(empty, c) : rank == 0 && !settled(full, c)) report_error(a.status, MOE_ERR_TIMEOUT, 61);
@@ -958,12 +998,14 @@ cudaError_t launch_ffn_forward(const FfnCall& c, int num_sms, cudaStream_t s) {
   a.p[0].ld = c.I;
   const bool few = c.T <= kRest;
   a.p[0].rest = few;
+  a.p[0].weights = 1;
   const Operands gu{c.x, c.T, c.H, c.w_gate_up, 2 * c.I, c.H};
   cudaError_t e = launch_products<EPI_GATED>(a, &gu, num_sms, s);
   if (e != cudaSuccess) return e;
   a.reset = 0;
   a.p[0] = problem(c.T, c.H, c.I, 0, 0, c.y);
   a.p[0].fold = few;
+  a.p[0].weights = 1;
   const Operands dn{h, few ? kRest + c.T : c.T, c.I, c.w_down, c.H, c.I};
   return launch_products<EPI_STORE>(a, &dn, num_sms, s);
 }
@@ -1000,6 +1042,7 @@ cudaError_t launch_ffn_backward(const FfnCall& c, int num_sms, cudaStream_t s) {
   if (c.dx) {
     op[n] = {dgu, rows, 2 * c.I, c.w_gate_up, 2 * c.I, c.H};
     p[n] = problem(c.T, c.H, 2 * c.I, 0, 1, c.dx);
+    p[n].weights = 1;
     p[n++].fold = few;
   }
   if (few && n > 0) {       // a launch of its own: its reduction is deep and split, the others' is 128
