@@ -459,7 +459,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const LinearArgs a)
         stage_scales<FMT, CB>(st + S::CODES, g, s0);
         stage_scales<FMT, CB>(st + S::CODES, g + 8, s1);
         const int nblk = min(CB, nb - chunk * CB);
-        // rows g and g + 8 share the swizzle; a stage's offset is a multiple of 128
+        // rows g and g + 8 share the swizzle; a stage starts on a multiple of its
+        // rows' length (of 128 bytes at 4 blocks), which the block's bits do not reach
         const uint32_t code0 = uint32_t(st - lsm) + lane_code;
         const int xc = (chunk - c_lo) * (CB * 64);
         // one scale for a whole stage of 4 blocks: their sums chain in the
